@@ -2,10 +2,11 @@
 NVIDIA B200 (sm_100a).
 
 The compute lives in ``libfc.so`` (C ABI declared in ``include/fc.h``,
-``include/fc_view.h`` and ``include/fc_state.h``); ``_lib`` is its ctypes
-binding and ``archive`` the host bookkeeping of one layer's compressed K/V
-streams (raw tail, capacity-doubling archive, reconstructed view, crop,
-batch gather, reset, save / restore) plus the multi-layer decode step.
+``include/fc_view.h``, ``include/fc_state.h`` and ``include/fc_paged.h``);
+``_lib`` is its ctypes binding, ``archive`` the host bookkeeping of one layer's
+compressed K/V streams (raw tail, capacity-doubling archive, reconstructed
+view, crop, batch gather, reset, save / restore) plus the multi-layer decode
+step, and ``paged`` the paged cache of sequences of different lengths.
 """
 
 from . import _lib
@@ -20,8 +21,10 @@ from ._lib import (FcArchive, FcError, FcTail, fc_append_step,
                    fc_state_restore)
 from .archive import (CodecKVCache, CodecStream, decode_step_layers,
                       grown_capacity)
+from .paged import PagedKVCache
 
 __all__ = [
+    "PagedKVCache",
     "CodecKVCache", "CodecStream", "decode_step_layers", "grown_capacity",
     "FcArchive", "FcTail", "FcError", "fc_compress_blocks", "fc_append_step",
     "fc_archive_copy_prefix", "fc_decode_plan", "fc_decode_workspace_bytes",

@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libfc (``include/fc.h``, ``include/fc_view.h``).
+"""Thin ctypes binding of libfc (``include/fc.h``, ``include/fc_view.h``,
+``include/fc_state.h``, ``include/fc_paged.h``).
 
 Argument marshalling only: tensors become device pointers, element strides
 and the current CUDA stream; every computation runs in libfc's kernels. A
@@ -46,7 +47,7 @@ FC_DTYPE_I8 = 2
 _DTYPE_CODE = {torch.float32: FC_DTYPE_F32, torch.bfloat16: FC_DTYPE_BF16,
                torch.int8: FC_DTYPE_I8}
 
-# Every symbol include/fc.h and include/fc_view.h declare.
+# Every symbol the headers of include/ declare.
 EXPORTS = (
     "fc_compress_blocks", "fc_append_step", "fc_archive_copy_prefix",
     "fc_decode_plan", "fc_decode_workspace_bytes", "fc_decode_attention",
@@ -56,6 +57,10 @@ EXPORTS = (
     "fc_decode_kernel", "fc_state_bytes", "fc_state_save", "fc_state_restore",
     "fc_decode_step_layers", "fc_decode_step_staging_bytes",
     "fc_decode_step_host",
+    "fc_pages_reset", "fc_pages_restore", "fc_pages_begin", "fc_pages_fork",
+    "fc_pages_free", "fc_pages_crop", "fc_pages_compact", "fc_paged_append",
+    "fc_paged_workspace_bytes", "fc_paged_attention", "fc_paged_step",
+    "fc_paged_read",
 )
 
 FC_MAX_LAYERS = 16
@@ -111,6 +116,30 @@ class FcTail(ctypes.Structure):
         ("data", ctypes.c_void_p), ("dtype", ctypes.c_int32),
         ("len", ctypes.c_int32), ("stride_b", ctypes.c_int64),
         ("stride_h", ctypes.c_int64),
+    ]
+
+
+class FcPages(ctypes.Structure):
+    """fc_pages of include/fc_paged.h."""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("n_layers", ctypes.c_int64), ("n_pages", ctypes.c_int64),
+        ("H", ctypes.c_int64), ("D", ctypes.c_int64),
+        ("stride_layer", ctypes.c_int64), ("stride_page", ctypes.c_int64),
+        ("stride_head", ctypes.c_int64),
+        ("scale_stride_layer", ctypes.c_int64),
+        ("scale_stride_page", ctypes.c_int64),
+        ("scale_stride_head", ctypes.c_int64),
+        ("n_slots", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+        ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+        ("batch", ctypes.c_void_p),
+        ("h_table", ctypes.c_void_p), ("h_lens", ctypes.c_void_p),
+        ("h_refs", ctypes.c_void_p),
+        ("first_free", ctypes.c_int64), ("n_free", ctypes.c_int64),
+        ("n_rows", ctypes.c_int64), ("n_tokens", ctypes.c_int64),
+        ("one_each", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
 
 
@@ -181,6 +210,28 @@ def load() -> ctypes.CDLL:
         "fc_crop": (ctypes.c_int, [PA, PT, I64, P]),
         "fc_select_batch": (ctypes.c_int, [PA, PT, PI64, I64, PA, PT, P]),
     }
+    PP = ctypes.POINTER(FcPages)
+    SZ, F32 = ctypes.c_size_t, ctypes.c_float
+    sig.update({
+        "fc_pages_reset": (ctypes.c_int, [PP, P]),
+        "fc_pages_restore": (ctypes.c_int, [PP, P, P, P]),
+        "fc_pages_begin": (ctypes.c_int, [PP, P, P, I64, I64, P]),
+        "fc_pages_fork": (ctypes.c_int, [PP, P, P, I64, P]),
+        "fc_pages_free": (ctypes.c_int, [PP, P, I64, P]),
+        "fc_pages_crop": (ctypes.c_int, [PP, I32, I64, P]),
+        "fc_pages_compact": (ctypes.c_int, [PP, PI64, P]),
+        "fc_paged_append": (ctypes.c_int, [PP, I64, P, P, I32, P, P, I64, I64,
+                                           P]),
+        "fc_paged_workspace_bytes": (SZ, [I64, I64, I64]),
+        "fc_paged_attention": (ctypes.c_int, [PP, I64, P, I32, P, I64, F32,
+                                              I64, I64, P, SZ, P, I32, P, P,
+                                              P]),
+        "fc_paged_step": (ctypes.c_int, [PP, I64, P, I32, P, I64, P, P, I32,
+                                         P, P, F32, I64, I64, P, SZ, P, I32,
+                                         P, P, P]),
+        "fc_paged_read": (ctypes.c_int, [PP, I64, I64, P, P, I32, P, P, I64,
+                                         P]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -556,3 +607,107 @@ def fc_select_batch(src: FcArchive, src_tail: Optional[FcTail], idx,
                                 len(idx), ctypes.byref(dst), _ref(dst_tail),
                                 s)
     _check(st, "fc_select_batch")
+
+
+# ------------------------------------------------------------- paged cache
+
+def _raw_stream(stream, device) -> int:
+    """cudaStream_t of the given stream, or torch's current one on device."""
+    if stream is not None:
+        return int(getattr(stream, "cuda_stream", stream))
+    if device.type != "cuda":
+        return 0
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _i32(values):
+    return None if values is None else \
+        (ctypes.c_int32 * max(1, len(values)))(*values)
+
+
+def fc_pages_reset(pages: FcPages, stream: int) -> None:
+    _check(load().fc_pages_reset(pages, stream), "fc_pages_reset")
+
+
+def fc_pages_restore(pages: FcPages, table: torch.Tensor, lens: torch.Tensor,
+                     stream: int) -> None:
+    _check(load().fc_pages_restore(pages, table.data_ptr(), lens.data_ptr(),
+                                   stream), "fc_pages_restore")
+
+
+def fc_pages_begin(pages: FcPages, slots, counts, n_rows: int,
+                   stream: int) -> None:
+    _check(load().fc_pages_begin(pages, _i32(slots), _i32(counts), len(slots),
+                                 n_rows, stream), "fc_pages_begin")
+
+
+def fc_pages_fork(pages: FcPages, src, dst, stream: int) -> None:
+    _check(load().fc_pages_fork(pages, _i32(src), _i32(dst), len(dst),
+                                stream), "fc_pages_fork")
+
+
+def fc_pages_free(pages: FcPages, slots, stream: int) -> None:
+    _check(load().fc_pages_free(pages, _i32(slots), len(slots), stream),
+           "fc_pages_free")
+
+
+def fc_pages_crop(pages: FcPages, slot: int, tokens_to_remove: int,
+                  stream: int) -> None:
+    _check(load().fc_pages_crop(pages, slot, tokens_to_remove, stream),
+           "fc_pages_crop")
+
+
+def fc_pages_compact(pages: FcPages, stream: int) -> int:
+    n = ctypes.c_int64(0)
+    _check(load().fc_pages_compact(pages, ctypes.byref(n), stream),
+           "fc_pages_compact")
+    return int(n.value)
+
+
+def fc_paged_append(pages: FcPages, layer: int, k: torch.Tensor,
+                    v: torch.Tensor, stream: int) -> None:
+    _check(load().fc_paged_append(
+        pages, layer, k.data_ptr(), v.data_ptr(), dtype_code(k.dtype),
+        _strides4(k), _strides4(v), k.shape[0], k.shape[2], stream),
+        "fc_paged_append")
+
+
+def fc_paged_workspace_bytes(Hq: int, H: int, D: int) -> int:
+    return int(load().fc_paged_workspace_bytes(Hq, H, D))
+
+
+def fc_paged_attention(pages: FcPages, layer: int, q: torch.Tensor,
+                       out: torch.Tensor, lse: Optional[torch.Tensor],
+                       softmax_scale: float, window: int, sinks: int,
+                       workspace: torch.Tensor, stream: int) -> None:
+    st = load().fc_paged_attention(
+        pages, layer, q.data_ptr(), _DTYPE_CODE[q.dtype], _strides4(q),
+        q.shape[1], softmax_scale, window, sinks, workspace.data_ptr(),
+        workspace.numel(), out.data_ptr(), _DTYPE_CODE[out.dtype],
+        _strides4(out), None if lse is None else lse.data_ptr(), stream)
+    if st != FC_OK:
+        raise FcError(st, "fc_paged_attention")
+
+
+def fc_paged_step(pages: FcPages, layer: int, q: torch.Tensor,
+                  k_new: torch.Tensor, v_new: torch.Tensor, out: torch.Tensor,
+                  lse: Optional[torch.Tensor], softmax_scale: float,
+                  window: int, sinks: int, workspace: torch.Tensor,
+                  stream: int) -> None:
+    st = load().fc_paged_step(
+        pages, layer, q.data_ptr(), _DTYPE_CODE[q.dtype], _strides4(q),
+        q.shape[1], k_new.data_ptr(), v_new.data_ptr(),
+        _DTYPE_CODE[k_new.dtype], _strides4(k_new), _strides4(v_new),
+        softmax_scale, window, sinks, workspace.data_ptr(),
+        workspace.numel(), out.data_ptr(), _DTYPE_CODE[out.dtype],
+        _strides4(out), None if lse is None else lse.data_ptr(), stream)
+    if st != FC_OK:
+        raise FcError(st, "fc_paged_step")
+
+
+def fc_paged_read(pages: FcPages, layer: int, slot: int, k_out: torch.Tensor,
+                  v_out: torch.Tensor, stream: int) -> None:
+    _check(load().fc_paged_read(
+        pages, layer, slot, k_out.data_ptr(), v_out.data_ptr(),
+        dtype_code(k_out.dtype), _strides4(k_out), _strides4(v_out),
+        k_out.shape[2], stream), "fc_paged_read")

@@ -1,0 +1,395 @@
+// The paged cache's data calls: append, read, and the host side of attention
+// and the fused step. Declared in include/fc_paged.h.
+#include <climits>
+
+#include "fc_paged_attn.cuh"
+
+namespace fc {
+namespace {
+
+constexpr int kTokens = 8;  // new tokens per CTA of the append
+constexpr int kAppendThreads = 256;
+
+struct AppendArgs {
+  PageView pages;
+  TokenView k, v;
+  int32_t dtype, vec;
+  int64_t M, offered;  // tokens per batch entry of the source, B * M
+};
+
+// The page row of new token n of the open batch, in rows of D elements from
+// the pool's head 0 (-1: none). Rows are found by their first token.
+__device__ __forceinline__ bool locate_token(const PageView& p, int64_t n, int32_t* page, int32_t* in) {
+  int lo = 0, hi = p.n_rows;  // the last row with first <= n
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.batch[mid].first <= n) lo = mid;
+    else hi = mid;
+  }
+  const BatchRow b = p.batch[lo];
+  if (b.slot < 0 || n < b.first || n >= int64_t(b.first) + b.count) return false;
+  const int32_t pos = b.len - b.count + int32_t(n - b.first);
+  if (pos < 0) return false;
+  *page = page_of(p, b.slot, pos);
+  *in = pos & ((1 << p.log2P) - 1);
+  return *page >= 0;
+}
+
+// bf16 and fp32 pages: a pass of 16-byte moves (read + write, HBM-bound). A CTA
+// takes 8 tokens of all heads, K and V; its source loads are issued before the
+// pages are known, four per thread at a time.
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int V = D * int(sizeof(T)) / 16;       // 16-byte words per row
+  constexpr int kRows = kAppendThreads / V;        // rows in flight per pass
+  __shared__ int32_t page[kTokens], in[kTokens];
+  const int64_t n0 = int64_t(blockIdx.x) * kTokens;
+  const int group = int(threadIdx.x) / V, w = int(threadIdx.x) % V;
+  const int H = a.pages.H, rows = kTokens * 2 * H;
+  bool placed = false;
+  for (int base = 0; base < rows; base += 4 * kRows) {
+    uint4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = base + u * kRows + group, tok = row / (2 * H), kv = row / H & 1, h = row % H;
+      const int64_t n = n0 + tok;
+      if (row >= rows || n >= a.offered) continue;
+      const TokenView& s = kv ? a.v : a.k;
+      const T* p = static_cast<const T*>(s.p) + n / a.M * s.sb + n % a.M * s.sm + h * s.sh;
+      if (a.vec) {
+        x[u] = __ldcs(reinterpret_cast<const uint4*>(p) + w);
+      } else {
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (sizeof(T) == 4) {
+            y[e] = __float_as_uint(p[w * 4 + e]);
+          } else {
+            const unsigned short* q = reinterpret_cast<const unsigned short*>(p) + w * 8 + 2 * e;
+            y[e] = uint32_t(q[0]) | uint32_t(q[1]) << 16;
+          }
+        }
+        x[u] = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    }
+    if (!placed) {
+      if (threadIdx.x < kTokens) {
+        int32_t g = -1, i = 0;
+        if (n0 + threadIdx.x >= a.offered || !locate_token(a.pages, n0 + threadIdx.x, &g, &i)) g = -1;
+        page[threadIdx.x] = g;
+        in[threadIdx.x] = i;
+      }
+      __syncthreads();
+      placed = true;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = base + u * kRows + group, tok = row / (2 * H), kv = row / H & 1, h = row % H;
+      if (row >= rows || page[tok] < 0) continue;
+      T* d = reinterpret_cast<T*>(kv ? a.pages.v : a.pages.k) + page[tok] * a.pages.stride_page +
+             h * a.pages.stride_head + int64_t(in[tok]) * D;
+      reinterpret_cast<uint4*>(d)[w] = x[u];
+    }
+  }
+}
+
+// int8 pages: a warp per row (token, head, K or V); see quantise_row.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) append_i8_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ int32_t page[kTokens], in[kTokens];
+  const int64_t n0 = int64_t(blockIdx.x) * kTokens;
+  if (threadIdx.x < kTokens) {
+    int32_t g = -1, i = 0;
+    if (n0 + threadIdx.x >= a.offered || !locate_token(a.pages, n0 + threadIdx.x, &g, &i)) g = -1;
+    page[threadIdx.x] = g;
+    in[threadIdx.x] = i;
+  }
+  __syncthreads();
+  const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+  const int H = a.pages.H, rows = kTokens * 2 * H;
+  for (int row = warp; row < rows; row += kAppendThreads / 32) {
+    const int tok = row / (2 * H), kv = row / H & 1, h = row % H;
+    if (page[tok] < 0) continue;
+    const int64_t n = n0 + tok;
+    const TokenView& s = kv ? a.v : a.k;
+    int8_t* d = reinterpret_cast<int8_t*>(kv ? a.pages.v : a.pages.k) + page[tok] * a.pages.stride_page +
+                h * a.pages.stride_head + int64_t(in[tok]) * D;
+    float* sc = (kv ? a.pages.vs : a.pages.ks) + page[tok] * a.pages.sstride_page +
+                h * a.pages.sstride_head + in[tok];
+    store_token_row<int8_t, D>(s.p, n / a.M * s.sb + n % a.M * s.sm + h * s.sh, a.dtype, a.vec, d, sc, lane);
+  }
+}
+
+struct ReadArgs {
+  PageView pages;
+  void* k;
+  void* v;
+  int64_t ks_h, ks_t, vs_h, vs_t;
+  int32_t slot, len;
+};
+
+// Dense rows of one slot: eight elements per thread and load, four rows in
+// flight; bound by HBM (pages read + rows written).
+template <typename T, typename TO, int D>
+__global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__ ReadArgs a) {
+  constexpr int V = D / 8, kRows = 256 / V, E = 8;
+  const int group = int(threadIdx.x) / V, w = int(threadIdx.x) % V;
+  const int h = int(blockIdx.y) >> 1, kv = int(blockIdx.y) & 1;
+  const int32_t t0 = int32_t(blockIdx.x) * (4 * kRows) + group;
+  float x[4][E];
+  bool on[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int32_t t = t0 + u * kRows;
+    const int32_t g = t < a.len ? page_of(a.pages, a.slot, t) : -1;
+    on[u] = g >= 0;
+    if (!on[u]) continue;
+    const int32_t in = t & ((1 << a.pages.log2P) - 1);
+    const T* p = reinterpret_cast<const T*>(kv ? a.pages.v : a.pages.k) + g * a.pages.stride_page +
+                 h * a.pages.stride_head + int64_t(in) * D + w * E;
+    load_vec<T, E>(p, x[u]);
+    if constexpr (sizeof(T) == 1) {
+      const float s = (kv ? a.pages.vs : a.pages.ks)[g * a.pages.sstride_page + h * a.pages.sstride_head + in];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[u][e] *= s;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (!on[u]) continue;
+    const int64_t t = t0 + u * kRows;
+    TO* o = static_cast<TO*>(kv ? a.v : a.k) + h * (kv ? a.vs_h : a.ks_h) + t * (kv ? a.vs_t : a.ks_t) + w * E;
+    if constexpr (sizeof(TO) == 4) {
+      reinterpret_cast<float4*>(o)[0] = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
+      reinterpret_cast<float4*>(o)[1] = make_float4(x[u][4], x[u][5], x[u][6], x[u][7]);
+    } else {
+      uint4 y;
+      y.x = pack_bf16(x[u][0], x[u][1]);
+      y.y = pack_bf16(x[u][2], x[u][3]);
+      y.z = pack_bf16(x[u][4], x[u][5]);
+      y.w = pack_bf16(x[u][6], x[u][7]);
+      *reinterpret_cast<uint4*>(o) = y;
+    }
+  }
+}
+
+template <int D>
+int launch_append(const AppendArgs& a, int pages_dtype, unsigned grid, cudaStream_t s) {
+  if (pages_dtype == FC_DTYPE_I8) append_i8_kernel<D><<<grid, kAppendThreads, 0, s>>>(a);
+  else if (pages_dtype == FC_DTYPE_F32) append_copy_kernel<float, D><<<grid, kAppendThreads, 0, s>>>(a);
+  else append_copy_kernel<__nv_bfloat16, D><<<grid, kAppendThreads, 0, s>>>(a);
+  return cuda_status(cudaGetLastError());
+}
+
+template <typename T, int D>
+int launch_read(const ReadArgs& a, int out_dtype, cudaStream_t s) {
+  const unsigned tile = 4 * 256 / (D / 8);
+  const dim3 grid((unsigned(a.len) + tile - 1) / tile, unsigned(a.pages.H) * 2);
+  if (out_dtype == FC_DTYPE_F32) paged_read_kernel<T, float, D><<<grid, 256, 0, s>>>(a);
+  else paged_read_kernel<T, __nv_bfloat16, D><<<grid, 256, 0, s>>>(a);
+  return cuda_status(cudaGetLastError());
+}
+
+template <int D>
+int launch_read_dtype(const ReadArgs& a, int dtype, int out_dtype, cudaStream_t s) {
+  if (dtype == FC_DTYPE_I8) return launch_read<int8_t, D>(a, out_dtype, s);
+  if (dtype == FC_DTYPE_F32) return launch_read<float, D>(a, out_dtype, s);
+  return launch_read<__nv_bfloat16, D>(a, out_dtype, s);
+}
+
+bool float_dtype(int32_t dt) { return dt == FC_DTYPE_F32 || dt == FC_DTYPE_BF16; }
+
+// Aligned for accesses of `bytes`: base and every stride (elements of size es).
+bool aligned_for(const void* p, const int64_t* st, int n, int64_t es, int64_t bytes) {
+  if (reinterpret_cast<uintptr_t>(p) % uintptr_t(bytes)) return false;
+  for (int i = 0; i < n; ++i)
+    if (st[i] * es % bytes) return false;
+  return true;
+}
+
+int check_layer(const fc_pages* p, int64_t layer) {
+  const int st = check_pages(p);
+  if (st != FC_OK) return st;
+  return layer < 0 || layer >= p->n_layers ? FC_ERR_INVALID : FC_OK;
+}
+
+// Tokens written to pages of p: their dtype is the pages', or any for int8.
+bool token_dtype_ok(const fc_pages* p, int32_t dtype) {
+  return float_dtype(dtype) && (p->dtype == FC_DTYPE_I8 || p->dtype == dtype);
+}
+
+struct PagedWorkspace {
+  size_t tickets, partials, total;
+};
+PagedWorkspace paged_workspace(int64_t D, int64_t G) {
+  const size_t ctas = size_t(sm_count()) * kPagedCtasPerSm;
+  PagedWorkspace w;
+  w.tickets = 0;
+  w.partials = pad256(ctas * 4);
+  w.total = w.partials + 2 * ctas * paged_fragment_bytes(D, G);
+  return w;
+}
+
+int attention(const fc_pages* p, int64_t layer, const void* q, int32_t q_dtype, const int64_t* q_strides,
+              int64_t Hq, bool step, const void* k_new, const void* v_new, int32_t new_dtype,
+              const int64_t* k_strides, const int64_t* v_strides, float softmax_scale, int64_t window,
+              int64_t sinks, void* workspace, size_t workspace_bytes, void* out, int32_t out_dtype,
+              const int64_t* out_strides, float* lse, fc_stream stream) {
+  const int st = check_layer(p, layer);
+  if (st != FC_OK) return st;
+  if (!q || !q_strides || !out || !out_strides || !workspace) return FC_ERR_INVALID;
+  if (!float_dtype(q_dtype) || !float_dtype(out_dtype)) return FC_ERR_INVALID;
+  if (q_strides[3] != 1 || out_strides[3] != 1 || window < 0 || sinks < 0) return FC_ERR_INVALID;
+  if (softmax_scale != softmax_scale || Hq < 1 || Hq % p->H) return FC_ERR_INVALID;
+  if (!paged_group_ok(Hq, p->H)) return FC_ERR_UNSUPPORTED;
+  if (p->n_rows < 1 || p->n_rows > p->n_slots) return FC_ERR_INVALID;
+  const int64_t q_es = dtype_size(q_dtype), o_es = dtype_size(out_dtype);
+  if (reinterpret_cast<uintptr_t>(q) % uintptr_t(q_es) || reinterpret_cast<uintptr_t>(out) % uintptr_t(o_es) ||
+      reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(workspace) % 256)
+    return FC_ERR_INVALID;
+  const int64_t G = Hq / p->H;
+  const PagedWorkspace ws = paged_workspace(p->D, G);
+  if (workspace_bytes < ws.total) return FC_ERR_INVALID;
+  PagedArgs a{};
+  if (step) {
+    if (!k_new || !v_new || !k_strides || !v_strides || !token_dtype_ok(p, new_dtype)) return FC_ERR_INVALID;
+    if (k_strides[3] != 1 || v_strides[3] != 1 || !p->one_each) return FC_ERR_INVALID;
+    const int64_t es = dtype_size(new_dtype), bytes = es * p->D / 32 > 16 ? 16 : es * p->D / 32;
+    if (reinterpret_cast<uintptr_t>(k_new) % uintptr_t(es) || reinterpret_cast<uintptr_t>(v_new) % uintptr_t(es))
+      return FC_ERR_INVALID;
+    a.kn = TokenView{k_new, k_strides[0], k_strides[1], 0};
+    a.vn = TokenView{v_new, v_strides[0], v_strides[1], 0};
+    a.new_dtype = new_dtype;
+    a.new_vec = (aligned_for(k_new, k_strides, 2, es, bytes) ? 1 : 0) |
+                (aligned_for(v_new, v_strides, 2, es, bytes) ? 2 : 0);
+  }
+  a.pages = page_view(p, layer);
+  a.q = TokenView{q, q_strides[0], q_strides[1], 0};
+  a.q_dtype = q_dtype;
+  a.q_vec = aligned_for(q, q_strides, 2, q_es, 4 * q_es) ? 1 : 0;
+  a.out_vec = aligned_for(out, out_strides, 2, o_es, 2 * o_es) ? 1 : 0;
+  a.G = int32_t(G);
+  a.q_limbs = q_dtype == FC_DTYPE_F32 ? 3 : 1;
+  a.p_limbs = out_dtype == FC_DTYPE_F32 ? 3 : 2;
+  const double sigma = softmax_scale > 0.0f ? double(softmax_scale) : 1.0 / sqrt(double(p->D));
+  a.scale_log2e = float(sigma * 1.4426950408889634);
+  a.window = int32_t(window < INT_MAX ? window : INT_MAX);
+  a.sinks = int32_t(sinks < INT_MAX - kTile ? sinks : INT_MAX - kTile);
+  a.out = out;
+  a.os_b = out_strides[0];
+  a.os_h = out_strides[1];
+  a.out_dtype = out_dtype;
+  a.lse = lse;
+  a.tickets = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + ws.tickets);
+  a.partials = static_cast<char*>(workspace) + ws.partials;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p->dtype == FC_DTYPE_I8) return launch_paged_attention_i8(a, p->D, s);
+  if (p->dtype == FC_DTYPE_F32) return launch_paged_attention_f32(a, p->D, s);
+  return launch_paged_attention_bf16(a, p->D, s);
+}
+
+}  // namespace
+}  // namespace fc
+
+using namespace fc;
+
+extern "C" int fc_paged_append(const fc_pages* p, int64_t layer, const void* k, const void* v, int32_t dtype,
+                               const int64_t* k_strides, const int64_t* v_strides, int64_t B, int64_t M,
+                               fc_stream stream) {
+  const int st = check_layer(p, layer);
+  if (st != FC_OK) return st;
+  if (p->n_rows < 1 || p->n_rows > p->n_slots || B < 0 || M < 0 || !token_dtype_ok(p, dtype))
+    return FC_ERR_INVALID;
+  if ((M > 0 && B > INT_MAX / M) || B * M < p->n_tokens) return FC_ERR_INVALID;
+  if (p->n_tokens == 0) return FC_OK;
+  if (!k || !v || !k_strides || !v_strides || k_strides[3] != 1 || v_strides[3] != 1) return FC_ERR_INVALID;
+  const int64_t es = dtype_size(dtype);
+  if (reinterpret_cast<uintptr_t>(k) % uintptr_t(es) || reinterpret_cast<uintptr_t>(v) % uintptr_t(es))
+    return FC_ERR_INVALID;
+  AppendArgs a{};
+  a.pages = page_view(p, layer);
+  a.k = TokenView{k, k_strides[0], k_strides[1], k_strides[2]};
+  a.v = TokenView{v, v_strides[0], v_strides[1], v_strides[2]};
+  a.dtype = dtype;
+  a.vec = aligned_for(k, k_strides, 3, es, 16) && aligned_for(v, v_strides, 3, es, 16) ? 1 : 0;
+  a.M = M;
+  a.offered = B * M;
+  // the grid covers every offered token, so that a captured launch serves any
+  // later batch of as many
+  const unsigned grid = unsigned((B * M + kTokens - 1) / kTokens);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (p->D) {
+    case 32:
+      return launch_append<32>(a, p->dtype, grid, s);
+    case 64:
+      return launch_append<64>(a, p->dtype, grid, s);
+    case 128:
+      return launch_append<128>(a, p->dtype, grid, s);
+    default:
+      return launch_append<256>(a, p->dtype, grid, s);
+  }
+}
+
+extern "C" size_t fc_paged_workspace_bytes(int64_t Hq, int64_t H, int64_t D) {
+  if (!paged_group_ok(Hq, H) || !paged_dim_ok(D)) return 0;
+  return paged_workspace(D, Hq / H).total;
+}
+
+extern "C" int fc_paged_attention(const fc_pages* p, int64_t layer, const void* q, int32_t q_dtype,
+                                  const int64_t* q_strides, int64_t Hq, float softmax_scale, int64_t window,
+                                  int64_t sinks, void* workspace, size_t workspace_bytes, void* out,
+                                  int32_t out_dtype, const int64_t* out_strides, float* lse,
+                                  fc_stream stream) {
+  return attention(p, layer, q, q_dtype, q_strides, Hq, false, nullptr, nullptr, 0, nullptr, nullptr,
+                   softmax_scale, window, sinks, workspace, workspace_bytes, out, out_dtype, out_strides, lse,
+                   stream);
+}
+
+extern "C" int fc_paged_step(const fc_pages* p, int64_t layer, const void* q, int32_t q_dtype,
+                             const int64_t* q_strides, int64_t Hq, const void* k_new, const void* v_new,
+                             int32_t new_dtype, const int64_t* k_strides, const int64_t* v_strides,
+                             float softmax_scale, int64_t window, int64_t sinks, void* workspace,
+                             size_t workspace_bytes, void* out, int32_t out_dtype, const int64_t* out_strides,
+                             float* lse, fc_stream stream) {
+  return attention(p, layer, q, q_dtype, q_strides, Hq, true, k_new, v_new, new_dtype, k_strides, v_strides,
+                   softmax_scale, window, sinks, workspace, workspace_bytes, out, out_dtype, out_strides, lse,
+                   stream);
+}
+
+extern "C" int fc_paged_read(const fc_pages* p, int64_t layer, int64_t slot, void* k_out, void* v_out,
+                             int32_t out_dtype, const int64_t* k_strides, const int64_t* v_strides, int64_t T,
+                             fc_stream stream) {
+  const int st = check_layer(p, layer);
+  if (st != FC_OK) return st;
+  if (slot < 0 || slot >= p->n_slots || !float_dtype(out_dtype)) return FC_ERR_INVALID;
+  const int32_t len = p->h_lens[slot];
+  if (T < len) return FC_ERR_INVALID;
+  if (len == 0) return FC_OK;
+  if (!k_out || !v_out || !k_strides || !v_strides || k_strides[3] != 1 || v_strides[3] != 1)
+    return FC_ERR_INVALID;
+  const int64_t es = dtype_size(out_dtype);
+  if (!aligned_for(k_out, k_strides, 3, es, 16) || !aligned_for(v_out, v_strides, 3, es, 16))
+    return FC_ERR_INVALID;
+  if (p->H > 32767) return FC_ERR_UNSUPPORTED;
+  ReadArgs a{};
+  a.pages = page_view(p, layer);
+  a.k = k_out;
+  a.v = v_out;
+  a.ks_h = k_strides[1];
+  a.ks_t = k_strides[2];
+  a.vs_h = v_strides[1];
+  a.vs_t = v_strides[2];
+  a.slot = int32_t(slot);
+  a.len = len;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (p->D) {
+    case 32:
+      return launch_read_dtype<32>(a, p->dtype, out_dtype, s);
+    case 64:
+      return launch_read_dtype<64>(a, p->dtype, out_dtype, s);
+    case 128:
+      return launch_read_dtype<128>(a, p->dtype, out_dtype, s);
+    default:
+      return launch_read_dtype<256>(a, p->dtype, out_dtype, s);
+  }
+}

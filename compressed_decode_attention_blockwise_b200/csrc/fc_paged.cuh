@@ -1,0 +1,152 @@
+// Internal helpers of the paged cache's translation units (not part of the ABI).
+#pragma once
+
+#include "fc_internal.cuh"
+#include "fc_paged.h"
+
+namespace fc {
+
+// Host validation of a paged cache's descriptor (storage, map pointers).
+int check_pages(const fc_pages* p);
+// FC_ERR_INVALID while `stream` is being captured (bookkeeping is a host
+// decision that a replay could not repeat).
+int check_not_capturing(fc_stream stream);
+
+inline bool paged_group_ok(int64_t Hq, int64_t H) {
+  if (H < 1 || Hq < 1 || Hq % H) return false;
+  const int64_t g = Hq / H;
+  return g == 1 || g == 2 || g == 4 || g == 8 || g == 16;
+}
+inline bool paged_dim_ok(int64_t D) { return D == 32 || D == 64 || D == 128 || D == 256; }
+
+// One row of the open batch as the kernels read it.
+struct BatchRow {
+  int32_t slot, len, first, count;
+};
+
+// Where one layer's pages are, by value for the kernels (strides in elements).
+struct PageView {
+  char* k;
+  char* v;
+  float* ks;
+  float* vs;
+  int64_t stride_page, stride_head, sstride_page, sstride_head;
+  const int32_t* table;
+  const BatchRow* batch;
+  int32_t max_pages, n_pages, n_slots, n_rows, log2P, H;
+};
+PageView page_view(const fc_pages* p, int64_t layer);
+
+// A bf16 or fp32 input of (B, H, M, D) with element strides.
+struct TokenView {
+  const void* p;
+  int64_t sb, sh, sm;
+};
+
+// ------------------------------------------------------------------ device
+
+// The page that holds position t of a slot, -1 when the map has none (so that
+// a stale map masks the token instead of sending a load astray).
+__device__ __forceinline__ int32_t page_of(const PageView& a, int32_t slot, int32_t t) {
+  const int32_t i = t >> a.log2P;
+  if (uint32_t(slot) >= uint32_t(a.n_slots) || uint32_t(i) >= uint32_t(a.max_pages)) return -1;
+  const int32_t pg = a.table[int64_t(slot) * a.max_pages + i];
+  return uint32_t(pg) < uint32_t(a.n_pages) ? pg : -1;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void load_words(uint32_t* w, const void* p) {
+  // plain (coherent) loads: the fused step reads rows its own warp has stored
+  if constexpr (BYTES == 16) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p));
+  } else if constexpr (BYTES == 8) {
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+  } else {
+    static_assert(BYTES == 4, "load width");
+    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+  }
+}
+
+// int8: code = x / (absmax / 127) to nearest, ties to even. y = |x| (127 / absmax)
+// in fp32 decides it unless y lies within 2^-12 of a half-integer (its error is
+// below 127 * 2^-22); there the exact comparison of 254 |x| with
+// (2k + 1) absmax, both exact in fp64 (24 + 8 bits), decides.
+__device__ __forceinline__ int quantise_one(float x, float r, float top) {
+  const float y = fabsf(x) * r;
+  int c = __float2int_rn(y);
+  if (fabsf(y - float(c)) > 0.5f - 0.000244140625f) {
+    const int k = int(floorf(y));  // the border k + 1/2 is the near one
+    const double a = 254.0 * double(fabsf(x)), b = (2.0 * k + 1.0) * double(top);
+    c = a > b ? k + 1 : a < b ? k : k + (k & 1);
+  }
+  c = c > 127 ? 127 : c;
+  return x < 0.0f ? -c : c;
+}
+
+template <int E>
+__device__ __forceinline__ void quantise_row(const float (&x)[E], int8_t* dst, float* scale, int lane) {
+  float top = 0.0f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    top = fmaxf(top, fabsf(x[i]));
+    bad |= !(fabsf(x[i]) <= 3.402823466e+38f);
+  }
+  top = warp_max(top);
+  bad = __any_sync(0xffffffffu, bad);
+  // 127 / top overflows below 2^-121; such rows take the quotient in fp64
+  const bool tiny = top < 1e-36f;
+  const float r = bad || top == 0.0f ? 0.0f : __fdiv_rn(127.0f, top);
+  int8_t c[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    if (bad || top == 0.0f) {
+      c[i] = 0;
+    } else if (tiny) {
+      c[i] = int8_t(__double2int_rn(127.0 * double(x[i]) / double(top)));
+    } else {
+      c[i] = int8_t(quantise_one(x[i], r, top));
+    }
+  }
+  if constexpr (E == 1) {
+    dst[0] = c[0];
+  } else if constexpr (E == 2) {
+    *reinterpret_cast<char2*>(dst) = make_char2(c[0], c[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i)
+      reinterpret_cast<char4*>(dst)[i] = make_char4(c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]);
+  }
+  if (lane == 0) *scale = bad ? __int_as_float(0x7fc00000) : float(double(top) / 127.0);
+}
+
+// Stores one token row (D elements of bf16 or fp32 at src[elem ..]) of one kv
+// head as the pages hold it; one warp, lane l the elements [l D/32, (l+1) D/32).
+// vec: the row is aligned for vector loads of a lane's share.
+template <typename T, int D>
+__device__ __forceinline__ void store_token_row(const void* src, int64_t elem, int src_dtype, bool vec,
+                                                T* dst, float* scale, int lane) {
+  constexpr int E = D / 32;
+  float x[E];
+  if (vec && src_dtype == FC_DTYPE_BF16) {
+    load_vec<__nv_bfloat16, E>(static_cast<const __nv_bfloat16*>(src) + elem + lane * E, x);
+  } else if (vec) {
+    load_vec<float, E>(static_cast<const float*>(src) + elem + lane * E, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = load_any(src, elem + lane * E + i, src_dtype);
+  }
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) dst[lane * E + i] = x[i];
+  } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) dst[lane * E + i] = __float2bfloat16_rn(x[i]);
+  } else {
+    quantise_row<E>(x, dst + lane * E, scale, lane);
+  }
+}
+
+}  // namespace fc
