@@ -269,7 +269,7 @@ int attention(const fc_pages* p, int64_t layer, const void* q, int32_t q_dtype, 
   a.q_vec = aligned_for(q, q_strides, 2, q_es, 4 * q_es) ? 1 : 0;
   a.out_vec = aligned_for(out, out_strides, 2, o_es, 2 * o_es) ? 1 : 0;
   a.G = int32_t(G);
-  a.q_limbs = q_dtype == FC_DTYPE_F32 ? 3 : 1;
+  a.q_limbs = q_dtype != FC_DTYPE_F32 ? 1 : p->dtype == FC_DTYPE_I8 ? 2 : 3;
   a.p_limbs = out_dtype == FC_DTYPE_F32 ? 3 : 2;
   const double sigma = softmax_scale > 0.0f ? double(softmax_scale) : 1.0 / sqrt(double(p->D));
   a.scale_log2e = float(sigma * 1.4426950408889634);

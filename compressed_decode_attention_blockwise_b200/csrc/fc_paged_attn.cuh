@@ -21,11 +21,14 @@
 // in the loop; the next tile's K loads are issued once S is done, its V loads
 // once O is, so loads are in flight all the time.
 //
-// Precision. K and V codes of bf16 and int8 pages are exact in bf16. The query
-// is one bf16 limb, or three (24 bits) when it is fp32; P is split into two
-// limbs (2^-17) for a bf16 output and three for an fp32 one; fp32 pages are
-// split into three limbs, products below 2^-24 of the largest dropped. Maxima,
-// sums and accumulators are fp32. int8 scales multiply S and P in fp32.
+// Precision. bf16 rows are exact as they are; the query is one bf16 limb, or
+// three (24 bits) when it is fp32; P is split into two limbs (2^-17) for a bf16
+// output and three for an fp32 one; fp32 pages are split into three limbs,
+// products below 2^-24 of the largest dropped. int8 codes are exact in fp16,
+// which takes fewer instructions than bf16 and holds 11 bits a limb: the query
+// (brought to fp16's range by a power of two per head) is one limb, two when
+// it is fp32, and P times V's scale (by a power of two per warp) is two.
+// Maxima, sums and accumulators are fp32.
 //
 // Softmax: each warp keeps its own running maximum per head and raises it only
 // when a tile exceeds it by more than 2^8 (a vote); until then p <= 2^8 and the
@@ -39,6 +42,8 @@
 // a segment (an atomic ticket, no waiting) joins those in order. The result
 // does not depend on which CTA is last.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include <atomic>
 
@@ -68,7 +73,7 @@ int launch_paged_attention_f32(const PagedArgs& a, int64_t D, cudaStream_t s);
 int launch_paged_attention_i8(const PagedArgs& a, int64_t D, cudaStream_t s);
 
 // CTAs a launch may have (the workspace is sized for them).
-constexpr int kPagedCtasPerSm = 2;
+constexpr int kPagedCtasPerSm = 1;
 // Bytes of one fragment in the workspace.
 inline size_t paged_fragment_bytes(int64_t D, int64_t G) {
   const size_t nt = G > 8 ? 2 : 1;
@@ -95,8 +100,7 @@ struct PagedCfg {
   static constexpr int CH = kRegs <= 192 ? 1 : kRegs <= 256 ? 2 : 4;
   static constexpr bool kPrefetch = CH == 1;
   static constexpr int NQ = NT * D / 16;      // float4 accumulators per lane
-  static constexpr int WARPS = NQ >= 32 ? 4 : 8;
-  static constexpr int kBlocks = kRegs <= 104 ? 2 : 1;  // CTAs per SM
+  static constexpr int WARPS = NQ >= 32 ? 4 : kRegs <= 96 ? 12 : 8;
   static constexpr size_t kFragment = size_t(NQ) * 512 + NT * 64;
   static constexpr size_t q_bytes(int limbs) { return size_t(limbs) * NT * (D / 32) * 512; }
 };
@@ -109,6 +113,26 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <typename T>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+  if constexpr (sizeof(T) == 1) mma_f16(d, a0, a1, a2, a3, b0, b1);
+  else mma_bf16(d, a0, a1, a2, a3, b0, b1);
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// The exponent of a positive finite x (its floor of log2; subnormals -127).
+__device__ __forceinline__ int exponent_of(float x) { return int(__float_as_uint(x) >> 23) - 127; }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
@@ -123,14 +147,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return d;
 }
 
-// Exact int8 -> bf16 of two codes in bytes 0 and 2 of x: with b7 the low seven
-// bits and b8 the sign bit, code = (128 + b7) - (b8 ? 256 : 128), and both
-// terms are bf16 bit patterns 0x4300 | bits.
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t x) {
-  const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+// Two fp16 (lo in the low half), rounded to nearest even.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// Exact int8 -> fp16 of two codes: x holds 0x6400 | (code + 128) in each half,
+// the fp16 numbers 1024 + code + 128; 1152 is subtracted.
+__device__ __forceinline__ uint32_t codes_to_f16(uint32_t x) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The fp16 limb of (lo, hi), rounded to nearest, and what remains (exact).
+__device__ __forceinline__ uint32_t take_limb_f16(float& lo, float& hi) {
+  const uint32_t w = pack_f16(lo, hi);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  lo -= f.x;
+  hi -= f.y;
+  return w;
 }
 
 // The limb of (lo, hi) as packed bf16, and what remains. Truncation keeps eight
@@ -277,7 +314,7 @@ __device__ __forceinline__ void store_fragment(char* p, int q, int lane, const f
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, PagedCfg<T, D, NT>::kBlocks)
+__global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
     paged_attention_kernel(const __grid_constant__ PagedArgs a) {
   using C = PagedCfg<T, D, NT>;
   constexpr int U = C::U, KW = C::KW, VW = C::VW, CH = C::CH, MT = D / 16;
@@ -349,42 +386,63 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, PagedCfg<T, D,
 
     // query fragments, pre-split into limbs, to this warp's shared memory
     __syncwarp();
-    {
-      const int64_t qb = row * a.q.sb;
+    float qf[NT][2];  // int8: what the scores of heads 2c and 2c + 1 are scaled by
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int g = nt * 8 + r;
-        const int64_t qh = qb + (int64_t(head) * a.G + g) * a.q.sh;
+    for (int nt = 0; nt < NT; ++nt) {
+      const int g = nt * 8 + r;
+      const int64_t qh = row * a.q.sb + (int64_t(head) * a.G + g) * a.q.sh;
+      float x[D / 32][8];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          const int idx = i * 8 + j, d = idx / C::KL * 4 * C::KL + c * C::KL + idx % C::KL;
+          float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (g < a.G) {
+            if (!a.q_vec) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] = load_any(a.q.p, qh + d + e, a.q_dtype);
+            } else if (a.q_dtype == FC_DTYPE_F32) {
+              load_vec<float, 4>(static_cast<const float*>(a.q.p) + qh + d, y);
+            } else {
+              load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16*>(a.q.p) + qh + d, y);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][j + e] = y[e];
+        }
+      if constexpr (C::ES == 1) {
+        // a power of two brings the head's largest |q| to [2^14, 2^15)
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // (0 and NaN rows, and infinities: any scale will do)
+        int e = top > 0.0f && top <= 3.402823466e+38f ? exponent_of(top) : 14;
+        e = e < -100 ? -100 : e;
+        const float up = pow2i(14 - e);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[i][k] *= up;
+        const float down = pow2i(e - 14);
+        qf[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c) * a.scale_log2e;
+        qf[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4) * a.scale_log2e;
+      }
+      for (int limb = 0; limb < a.q_limbs; ++limb)
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          float x[8];
+          uint32_t w[4];
 #pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            const int idx = i * 8 + j, d = idx / C::KL * 4 * C::KL + c * C::KL + idx % C::KL;
-            float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (g < a.G) {
-              if (!a.q_vec) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = load_any(a.q.p, qh + d + e, a.q_dtype);
-              } else if (a.q_dtype == FC_DTYPE_F32) {
-                load_vec<float, 4>(static_cast<const float*>(a.q.p) + qh + d, y);
-              } else {
-                load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16*>(a.q.p) + qh + d, y);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[j + e] = y[e];
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (C::ES == 1) w[e] = take_limb_f16(x[i][2 * e], x[i][2 * e + 1]);
+            else w[e] = take_limb(x[i][2 * e], x[i][2 * e + 1]);
           }
-          for (int limb = 0; limb < a.q_limbs; ++limb) {
-            uint4 w;
-            w.x = take_limb(x[0], x[1]);
-            w.y = take_limb(x[2], x[3]);
-            w.z = take_limb(x[4], x[5]);
-            w.w = take_limb(x[6], x[7]);
-            qs[((limb * NT + nt) * (D / 32) + i) * 32 + lane] = w;
-          }
+          qs[((limb * NT + nt) * (D / 32) + i) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-      }
     }
     const char* kh = pv.k + int64_t(head) * pv.stride_head * C::ES;
     const char* vh = pv.v + int64_t(head) * pv.stride_head * C::ES;
@@ -413,20 +471,40 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, PagedCfg<T, D,
       m[nt][0] = m[nt][1] = __int_as_float(0xff800000);
       l[nt][0] = l[nt][1] = 0.0f;
     }
+    int ve = 0;                                       // int8: see below
+    float v_most = -1.0f, v_mul = 0.0f, svc[U][2];
 
-    uint32_t kr[U][2][KW / CH], vr[U][4][VW / CH];
-    int32_t pg[U][2], npg[U][2];      // pages of the tiles' two halves
-    float sk[U][2], sv[U][2];         // int8: scales of tokens r and r + 8
+    uint32_t kr[U][2][KW / CH] = {}, vr[U][4][VW / CH] = {};
+    int32_t pg[U][2];                 // pages of the tiles' two halves
+    float sk[U][2] = {}, sv[U][2] = {};  // int8: scales of tokens r and r + 8
+    bool full;                        // every token of the iteration is seen
 
     const int32_t Pm = (1 << pv.log2P) - 1;
-    auto pages_of = [&](int32_t i, int32_t (&g)[U][2]) {
+    // The table ahead of its use: lane j holds the pages of tiles `held` + j
+    // (a page of 8 tokens holds half a tile) and of the 32 tiles after them.
+    int32_t held = tile, cur[2], nxt[2];
+    auto fetch = [&](int32_t i, int32_t (&g)[2]) {
+      const int32_t t = rt.start(i + lane);
+      const bool in = i + lane < end && t < rt.len;
+      g[0] = in ? page_of(pv, br.slot, t) : -1;
+      g[1] = pv.log2P > 3 ? g[0] : in && t + 8 < rt.len ? page_of(pv, br.slot, t + 8) : -1;
+    };
+    fetch(held, cur);
+    fetch(held + 32, nxt);
+    auto pages_of = [&](int32_t i) {
+      if (i - held == 32) {
+        held = i;
+        cur[0] = nxt[0];
+        cur[1] = nxt[1];
+        fetch(held + 32, nxt);
+      }
+      full = true;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        pg[u][0] = __shfl_sync(0xffffffffu, cur[0], i - held + u);
+        pg[u][1] = __shfl_sync(0xffffffffu, cur[1], i - held + u);
         const int32_t t = rt.start(i + u);
-        const bool in = i + u < end && t < rt.len;
-        g[u][0] = in ? page_of(pv, br.slot, t) : -1;
-        // a page of 8 tokens holds half a tile
-        g[u][1] = pv.log2P > 3 ? g[u][0] : in && t + 8 < rt.len ? page_of(pv, br.slot, t + 8) : -1;
+        full &= pg[u][0] >= 0 && pg[u][1] >= 0 && t + kTile <= rt.len && (t >= rt.lo || t + kTile <= rt.sinks);
       }
     };
     auto load_k = [&](int32_t i, int part) {
@@ -435,26 +513,18 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, PagedCfg<T, D,
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const int32_t t = rt.start(i + u) + hh * 8 + r;
-          const bool on = pg[u][hh] >= 0 && rt.sees(t);
           const char* p = kh + (pg[u][hh] * pv.stride_page + int64_t(t & Pm) * D) * C::ES + c * KB;
+          if (full || (pg[u][hh] >= 0 && rt.sees(t))) {
 #pragma unroll
-          for (int j = 0; j < KW / CH; j += KB / 4) {
-            if (on) {
+            for (int j = 0; j < KW / CH; j += KB / 4)
               load_words<KB>(&kr[u][hh][j], p + (j * 4 + part * (KW / CH) * 4) * 4);
-            } else {
-#pragma unroll
-              for (int e = 0; e < KB / 4; ++e) kr[u][hh][j + e] = 0;
+            if constexpr (C::ES == 1) {
+              const int64_t se = pg[u][hh] * pv.sstride_page + head * pv.sstride_head + (t & Pm);
+              load_words<4>(reinterpret_cast<uint32_t*>(&sk[u][hh]), pv.ks + se);
+              load_words<4>(reinterpret_cast<uint32_t*>(&sv[u][hh]), pv.vs + se);
             }
-          }
-          if constexpr (C::ES == 1) {
-            const int64_t se = pg[u][hh] * pv.sstride_page + head * pv.sstride_head + (t & Pm);
-            uint32_t w[2] = {0, 0};
-            if (on) {
-              load_words<4>(&w[0], pv.ks + se);
-              load_words<4>(&w[1], pv.vs + se);
-            }
-            sk[u][hh] = __uint_as_float(w[0]);
-            sv[u][hh] = __uint_as_float(w[1]);
+          } else if constexpr (C::ES == 1) {
+            sv[u][hh] = 0.0f;  // (a masked K row may hold anything: its score is replaced)
           }
         }
     };
@@ -464,28 +534,24 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, PagedCfg<T, D,
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int32_t g = pg[u][k >> 1], t = rt.start(i + u) + (k >> 1) * 8 + 2 * c + (k & 1);
-          const bool on = g >= 0 && rt.sees(t);
           const char* p = vh + (g * pv.stride_page + int64_t(t & Pm) * D) * C::ES + r * VB;
+          if (full || (g >= 0 && rt.sees(t))) {
 #pragma unroll
-          for (int j = 0; j < VW / CH; j += VB / 4) {
-            if (on) {
+            for (int j = 0; j < VW / CH; j += VB / 4)
               load_words<VB>(&vr[u][k][j], p + (j * 8 + part * (VW / CH) * 8) * 4);
-            } else {
+          } else {
 #pragma unroll
-              for (int e = 0; e < VB / 4; ++e) vr[u][k][j + e] = 0;
-            }
+            for (int j = 0; j < VW / CH; ++j) vr[u][k][j] = 0;
           }
         }
     };
 
-    pages_of(tile, pg);
+    pages_of(tile);
     if constexpr (C::kPrefetch) {
       load_k(tile, 0);
       load_v(tile, 0);
     }
     for (int32_t i = tile; i < end; i += U) {
-      if constexpr (C::kPrefetch) pages_of(i + U, npg);
-
       // ---- S^T = K Q^T
       float s[U][NT][4];
 #pragma unroll
@@ -526,32 +592,39 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, PagedCfg<T, D,
         } else {
           // bf16, int8: K is exact in one limb; the limbs of the query
           float odd[U][NT][4] = {};  // a second chain of dependent products
-          for (int ql = 0; ql < a.q_limbs; ++ql) {
 #pragma unroll
-            for (int ks = 0; ks < STEPS; ++ks)
+          for (int ks = 0; ks < STEPS; ++ks) {
+            const int kk = part * STEPS + ks;
+            uint32_t k0[U], k1[U], k2[U], k3[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              if constexpr (C::ES == 2) {
+                k0[u] = kr[u][0][2 * ks];
+                k1[u] = kr[u][1][2 * ks];
+                k2[u] = kr[u][0][2 * ks + 1];
+                k3[u] = kr[u][1][2 * ks + 1];
+              } else {
+                const uint32_t x0 = kr[u][0][ks] ^ 0x80808080u, x1 = kr[u][1][ks] ^ 0x80808080u;
+                k0[u] = codes_to_f16(__byte_perm(x0, 0x64646464u, 0x4140));
+                k1[u] = codes_to_f16(__byte_perm(x1, 0x64646464u, 0x4140));
+                k2[u] = codes_to_f16(__byte_perm(x0, 0x64646464u, 0x4342));
+                k3[u] = codes_to_f16(__byte_perm(x1, 0x64646464u, 0x4342));
+              }
+            }
+#pragma unroll
+            for (int ql = 0; ql < (C::ES == 1 ? 2 : 3); ++ql) {
+              if (ql >= a.q_limbs) break;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                const int kk = part * STEPS + ks;
                 const uint2 b = reinterpret_cast<const uint2*>(
                     &qs[((ql * NT + nt) * (D / 32) + kk / 2) * 32 + lane])[kk & 1];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                  uint32_t a0, a1, a2, a3;
-                  if constexpr (C::ES == 2) {
-                    a0 = kr[u][0][2 * ks];
-                    a1 = kr[u][1][2 * ks];
-                    a2 = kr[u][0][2 * ks + 1];
-                    a3 = kr[u][1][2 * ks + 1];
-                  } else {
-                    a0 = codes_to_bf16(__byte_perm(kr[u][0][ks], 0, 0x4140));
-                    a1 = codes_to_bf16(__byte_perm(kr[u][1][ks], 0, 0x4140));
-                    a2 = codes_to_bf16(__byte_perm(kr[u][0][ks], 0, 0x4342));
-                    a3 = codes_to_bf16(__byte_perm(kr[u][1][ks], 0, 0x4342));
-                  }
-                  if (ks & 1) mma_bf16(odd[u][nt], a0, a1, a2, a3, b.x, b.y);
-                  else mma_bf16(s[u][nt], a0, a1, a2, a3, b.x, b.y);
+                  if (ks & 1) mma<T>(odd[u][nt], k0[u], k1[u], k2[u], k3[u], b.x, b.y);
+                  else mma<T>(s[u][nt], k0[u], k1[u], k2[u], k3[u], b.x, b.y);
                 }
               }
+            }
           }
 #pragma unroll
           for (int u = 0; u < U; ++u)
@@ -566,27 +639,52 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, PagedCfg<T, D,
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const bool on = pg[u][hh] >= 0 && rt.sees(rt.start(i + u) + hh * 8 + r);
-          float f = a.scale_log2e;
-          if constexpr (C::ES == 1) f *= sk[u][hh];
+        for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              s[u][nt][2 * hh + j] = on ? s[u][nt][2 * hh + j] * f : __int_as_float(0xff800000);
-        }
-      float svc[U][2];  // this iteration's V scales, before the prefetch
-      if constexpr (C::ES == 1) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) svc[u][0] = sv[u][0], svc[u][1] = sv[u][1];
-      }
-      if constexpr (C::kPrefetch) {
-        int32_t hold[U][2];
+            for (int j = 0; j < 2; ++j) {
+              if constexpr (C::ES == 1) s[u][nt][2 * hh + j] *= sk[u][hh] * qf[nt][j];
+              else s[u][nt][2 * hh + j] *= a.scale_log2e;
+            }
+      if (!full) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) hold[u][hh] = pg[u][hh], pg[u][hh] = npg[u][hh], npg[u][hh] = hold[u][hh];
+          for (int hh = 0; hh < 2; ++hh) {
+            if (pg[u][hh] >= 0 && rt.sees(rt.start(i + u) + hh * 8 + r)) continue;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              s[u][nt][2 * hh] = s[u][nt][2 * hh + 1] = __int_as_float(0xff800000);
+          }
+      }
+      if constexpr (C::ES == 1) {
+        // V's scales are multiplied into P as 2^(7 - ve) scale, ve above the
+        // exponent of every scale so far, so that fp16 holds them (p <= 2^8)
+        float x = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) x = fmaxf(x, fmaxf(sv[u][0], sv[u][1]));
+        if (__any_sync(0xffffffffu, x > v_most)) {
+          x = warp_max(x);
+          int e = exponent_of(x) + 1;
+          e = e < -100 ? -100 : e > 120 ? 120 : e;
+          const float f = v_most < 0.0f ? 0.0f : pow2i(ve - e < -126 ? -126 : ve - e);
+          ve = e;
+          v_most = pow2i(e);
+          v_mul = pow2i(7 - e);
+#pragma unroll
+          for (int q = 0; q < C::NQ; ++q)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[q][k] *= f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          svc[u][0] = sv[u][0] * v_mul;  // before the prefetch
+          svc[u][1] = sv[u][1] * v_mul;
+        }
+      }
+      if constexpr (C::kPrefetch) {
+        pages_of(i + U);
         load_k(i + U, 0);
       }
 
@@ -642,21 +740,27 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, PagedCfg<T, D,
             }
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
+              if constexpr (C::ES == 1) {
+                if (k < 2) pb[u][k][nt][hh] = transpose8x8(take_limb_f16(p[0], p[1]));
+                continue;
+              }
               // the last limb is rounded, the ones before keep eight bits each
               if (k < a.p_limbs - 1) pb[u][k][nt][hh] = transpose8x8(take_limb(p[0], p[1]));
               else if (k < a.p_limbs) pb[u][k][nt][hh] = transpose8x8(pack_bf16(p[0], p[1]));
             }
           }
 
-      // ---- O^T += V^T P^T
+      // ---- O^T += V^T P^T: the iteration's products in accumulators of their
+      // own, added in fp32 (the tensor cores' running sums are truncated)
 #pragma unroll
       for (int part = 0; part < CH; ++part) {
         if constexpr (!C::kPrefetch) load_v(i, part);
 #pragma unroll
-        for (int mt = 0; mt < MT / CH; ++mt)
+        for (int mt = 0; mt < MT / CH; ++mt) {
+          const int q = part * (MT / CH) + mt;
+          float o[NT][4] = {};
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int q = part * (MT / CH) + mt;
             if constexpr (C::ES == 4) {
               float x[4][2];
 #pragma unroll
@@ -672,7 +776,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, PagedCfg<T, D,
                   if (k < a.p_limbs) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                      mma_bf16(acc[nt * MT + q], a0, a1, a2, a3, pb[u][k][nt][0], pb[u][k][nt][1]);
+                      mma_bf16(o[nt], a0, a1, a2, a3, pb[u][k][nt][0], pb[u][k][nt][1]);
                   }
               }
             } else {
@@ -685,23 +789,32 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, PagedCfg<T, D,
               } else {
                 // codes 2 mt and 2 mt + 1 of each token: bytes of word mt / 2
                 const uint32_t lo = mt & 1 ? 0x0602u : 0x0400u, hi = mt & 1 ? 0x0703u : 0x0501u;
-                a0 = codes_to_bf16(__byte_perm(vr[u][0][mt / 2], vr[u][1][mt / 2], lo));
-                a1 = codes_to_bf16(__byte_perm(vr[u][0][mt / 2], vr[u][1][mt / 2], hi));
-                a2 = codes_to_bf16(__byte_perm(vr[u][2][mt / 2], vr[u][3][mt / 2], lo));
-                a3 = codes_to_bf16(__byte_perm(vr[u][2][mt / 2], vr[u][3][mt / 2], hi));
+                auto pair = [](uint32_t w0, uint32_t w1, uint32_t sel) {
+                  return codes_to_f16((__byte_perm(w0, w1, sel) & 0x00ff00ffu) ^ 0x64806480u);
+                };
+                a0 = pair(vr[u][0][mt / 2], vr[u][1][mt / 2], lo);
+                a1 = pair(vr[u][0][mt / 2], vr[u][1][mt / 2], hi);
+                a2 = pair(vr[u][2][mt / 2], vr[u][3][mt / 2], lo);
+                a3 = pair(vr[u][2][mt / 2], vr[u][3][mt / 2], hi);
               }
+              constexpr int kMost = C::ES == 1 ? 2 : 3;
 #pragma unroll
-              for (int k = 0; k < 3; ++k)
-                if (k < a.p_limbs) {
+              for (int k = 0; k < kMost; ++k)
+                if (C::ES == 1 || k < a.p_limbs) {
 #pragma unroll
                   for (int nt = 0; nt < NT; ++nt)
-                    mma_bf16(acc[nt * MT + q], a0, a1, a2, a3, pb[u][k][nt][0], pb[u][k][nt][1]);
+                    mma<T>(o[nt], a0, a1, a2, a3, pb[u][k][nt][0], pb[u][k][nt][1]);
                 }
             }
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nt * MT + q][e] += o[nt][e];
+        }
       }
       if constexpr (C::kPrefetch) load_v(i + U, 0);
-      else pages_of(i + U, pg);
+      else pages_of(i + U);
     }
 
     // ---- the segment's sums over the lanes' tokens; whole segments are done
@@ -711,6 +824,13 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, PagedCfg<T, D,
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], o);
+    if constexpr (C::ES == 1) {
+      const float f = v_most < 0.0f ? 0.0f : pow2i(ve - 7);
+#pragma unroll
+      for (int q = 0; q < C::NQ; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[q][k] *= f;
+    }
     const bool whole = tile == 0 && end == rt.n;
     char* frag = fragments + (warp * 2 + made) * C::kFragment;
 #pragma unroll
@@ -827,7 +947,7 @@ int launch_paged(const PagedArgs& a, cudaStream_t s) {
       return FC_ERR_CUDA;
     set[dev] = true;
   }
-  const unsigned grid = unsigned(sm_count() * (C::kBlocks < kPagedCtasPerSm ? C::kBlocks : kPagedCtasPerSm));
+  const unsigned grid = unsigned(sm_count() * kPagedCtasPerSm);
   kernel<<<grid, C::WARPS * 32, smem, s>>>(a);
   return cuda_status(cudaGetLastError());
 }
