@@ -266,11 +266,9 @@ int attention(const fc_pages* p, int64_t layer, const void* q, int32_t q_dtype, 
   a.pages = page_view(p, layer);
   a.q = TokenView{q, q_strides[0], q_strides[1], 0};
   a.q_dtype = q_dtype;
-  a.q_vec = aligned_for(q, q_strides, 2, q_es, 4 * q_es) ? 1 : 0;
+  a.q_vec = (aligned_for(q, q_strides, 2, q_es, 4 * q_es) ? 1 : 0) | (aligned_for(q, q_strides, 2, q_es, 16) ? 2 : 0);
   a.out_vec = aligned_for(out, out_strides, 2, o_es, 2 * o_es) ? 1 : 0;
   a.G = int32_t(G);
-  a.q_limbs = q_dtype != FC_DTYPE_F32 ? 1 : p->dtype == FC_DTYPE_I8 ? 2 : 3;
-  a.p_limbs = out_dtype == FC_DTYPE_F32 ? 3 : 2;
   const double sigma = softmax_scale > 0.0f ? double(softmax_scale) : 1.0 / sqrt(double(p->D));
   a.scale_log2e = float(sigma * 1.4426950408889634);
   a.window = int32_t(window < INT_MAX ? window : INT_MAX);
@@ -283,9 +281,13 @@ int attention(const fc_pages* p, int64_t layer, const void* q, int32_t q_dtype, 
   a.tickets = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + ws.tickets);
   a.partials = static_cast<char*>(workspace) + ws.partials;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p->dtype == FC_DTYPE_I8) return launch_paged_attention_i8(a, p->D, s);
-  if (p->dtype == FC_DTYPE_F32) return launch_paged_attention_f32(a, p->D, s);
-  return launch_paged_attention_bf16(a, p->D, s);
+  // limbs of (query, P): as many as the query's and the output's type need
+  const bool fine_q = q_dtype == FC_DTYPE_F32, fine_out = out_dtype == FC_DTYPE_F32;
+  if (p->dtype == FC_DTYPE_F32) return launch_paged_attention_f32_33(a, p->D, s);
+  if (p->dtype == FC_DTYPE_I8)
+    return fine_q ? launch_paged_attention_i8_22(a, p->D, s) : launch_paged_attention_i8_12(a, p->D, s);
+  if (fine_q) return launch_paged_attention_bf16_33(a, p->D, s);
+  return fine_out ? launch_paged_attention_bf16_13(a, p->D, s) : launch_paged_attention_bf16_12(a, p->D, s);
 }
 
 }  // namespace

@@ -57,7 +57,6 @@ struct PagedArgs {
   int32_t q_dtype, new_dtype;
   int32_t q_vec, new_vec, out_vec;  // aligned for vector access
   int32_t G;
-  int32_t q_limbs, p_limbs;
   float scale_log2e;
   int32_t window, sinks;
   void* out;
@@ -68,9 +67,12 @@ struct PagedArgs {
   char* partials;      // two fragments per CTA
 };
 
-int launch_paged_attention_bf16(const PagedArgs& a, int64_t D, cudaStream_t s);
-int launch_paged_attention_f32(const PagedArgs& a, int64_t D, cudaStream_t s);
-int launch_paged_attention_i8(const PagedArgs& a, int64_t D, cudaStream_t s);
+int launch_paged_attention_bf16_12(const PagedArgs& a, int64_t D, cudaStream_t s);
+int launch_paged_attention_bf16_13(const PagedArgs& a, int64_t D, cudaStream_t s);
+int launch_paged_attention_bf16_33(const PagedArgs& a, int64_t D, cudaStream_t s);
+int launch_paged_attention_f32_33(const PagedArgs& a, int64_t D, cudaStream_t s);
+int launch_paged_attention_i8_12(const PagedArgs& a, int64_t D, cudaStream_t s);
+int launch_paged_attention_i8_22(const PagedArgs& a, int64_t D, cudaStream_t s);
 
 // CTAs a launch may have (the workspace is sized for them).
 constexpr int kPagedCtasPerSm = 1;
@@ -85,9 +87,10 @@ inline size_t paged_fragment_bytes(int64_t D, int64_t G) {
 constexpr int kTile = 16;          // tokens per tile
 constexpr float kLazy = 8.0f;      // log2 of how far p may exceed 1
 
-template <typename T, int D_, int NT_>
+// QL, PL: limbs of the query and of P.
+template <typename T, int D_, int NT_, int QL_, int PL_>
 struct PagedCfg {
-  static constexpr int D = D_, NT = NT_;      // NT: groups of 8 heads
+  static constexpr int D = D_, NT = NT_, QL = QL_, PL = PL_;  // NT: groups of 8 heads
   static constexpr int ES = int(sizeof(T));
   static constexpr int KW = D / 4 * ES / 4;   // words of a K row per lane
   static constexpr int VW = D / 8 * ES / 4;   // words of a V row per lane
@@ -102,31 +105,26 @@ struct PagedCfg {
   static constexpr int NQ = NT * D / 16;      // float4 accumulators per lane
   static constexpr int WARPS = NQ >= 32 ? 4 : kRegs <= 96 ? 12 : 8;
   static constexpr size_t kFragment = size_t(NQ) * 512 + NT * 64;
-  static constexpr size_t q_bytes(int limbs) { return size_t(limbs) * NT * (D / 32) * 512; }
+  static constexpr size_t kQuery = size_t(QL) * NT * (D / 32) * 512;
+  static constexpr size_t kShared = WARPS * (2 * kFragment + kQuery);
 };
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-template <typename T>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                    uint32_t b0, uint32_t b1) {
-  if constexpr (sizeof(T) == 1) mma_f16(d, a0, a1, a2, a3, b0, b1);
-  else mma_bf16(d, a0, a1, a2, a3, b0, b1);
+// d += A B, or d = A B where FIRST (16 x 8 x 16; bf16, or fp16 for int8 pages).
+template <typename T, bool FIRST>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  const float c0 = FIRST ? 0.0f : d[0], c1 = FIRST ? 0.0f : d[1], c2 = FIRST ? 0.0f : d[2],
+              c3 = FIRST ? 0.0f : d[3];
+  if constexpr (sizeof(T) == 1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  }
 }
 
 // 2^e for -126 <= e <= 127.
@@ -189,8 +187,8 @@ __device__ __forceinline__ float fast_exp2(float x) {
 struct RowTiles {
   int32_t len, lo, sinks;  // seen: t < len and (t >= lo or t < sinks)
   int32_t ns, w0, n;       // tile i starts at 16 (i < ns ? i : i - ns + w0)
-  __device__ __forceinline__ RowTiles(int32_t slot, int32_t length, int32_t window, int32_t sink) {
-    len = slot < 0 ? 0 : length;
+  __device__ __forceinline__ RowTiles(const BatchRow& b, int32_t window, int32_t sink) {
+    len = b.slot < 0 ? 0 : b.len;
     lo = window > 0 && len > window ? len - window : 0;
     sinks = sink < lo ? sink : lo;
     ns = (sinks + kTile - 1) / kTile;
@@ -209,7 +207,7 @@ __device__ __forceinline__ float join_factor(float m, float M) { return m == M ?
 
 // Writes the (already joined) accumulator quad q of one lane: heads 8 nt + 2c
 // and + 1, channels d and d + 1 of D.
-template <typename C, typename T>
+template <typename C>
 __device__ __forceinline__ void store_quad(const PagedArgs& a, int32_t row, int32_t head, int q, int lane,
                                            const float (&acc)[4], const float (&l)[2]) {
   const int nt = q / (C::D / 16), mt = q % (C::D / 16), r = lane >> 2, c = lane & 3;
@@ -275,33 +273,6 @@ struct Piece {
   int32_t row, head, from, to, n;
 };
 
-// Joins n fragments (at(i)) for quad q: the lane's accumulators, maxima, sums.
-template <typename C, typename At>
-__device__ __forceinline__ void join(int n, At at, int q, int lane, float (&acc)[4], float (&m)[2],
-                                     float (&l)[2]) {
-  const int nt = q / (C::D / 16), c = lane & 3;
-  m[0] = m[1] = __int_as_float(0xff800000);
-  for (int i = 0; i < n; ++i) {
-    const float2 x = Fragment<C>{at(i)}.m(nt, c);
-    m[0] = fmaxf(m[0], x.x);
-    m[1] = fmaxf(m[1], x.y);
-  }
-  acc[0] = acc[1] = acc[2] = acc[3] = l[0] = l[1] = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const Fragment<C> f{at(i)};
-    const float2 mi = f.m(nt, c), li = f.l(nt, c);
-    const float4 v = f.acc(q, lane);
-    const float e0 = join_factor(mi.x, m[0]), e1 = join_factor(mi.y, m[1]);
-    l[0] += li.x * e0;
-    l[1] += li.y * e1;
-    acc[0] += v.x * e0;
-    acc[1] += v.y * e1;
-    acc[2] += v.z * e0;
-    acc[3] += v.w * e1;
-  }
-}
-
 template <typename C>
 __device__ __forceinline__ void store_fragment(char* p, int q, int lane, const float (&acc)[4],
                                                const float (&m)[2], const float (&l)[2]) {
@@ -313,28 +284,89 @@ __device__ __forceinline__ void store_fragment(char* p, int q, int lane, const f
   }
 }
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
+// Joins n fragments for quad q and stores the result, as the row's output (to
+// null) or as a fragment. Fragment i lies at base + kFragment * ids[i], or, in
+// the workspace (ids null), at first, first + 1, first + 3, ...: the segment's
+// first CTA left its second fragment, every later one its first.
+template <typename C>
+__device__ __noinline__ void join_quad(const PagedArgs& a, const char* base, const int* ids, int first, int n,
+                                       char* to, int32_t row, int32_t head, int q) {
+  const int lane = int(threadIdx.x & 31), nt = q / (C::D / 16), c = lane & 3;
+  auto at = [&](int i) {
+    return Fragment<C>{base + size_t(ids ? ids[i] : i == 0 ? first : first + 2 * i - 1) * C::kFragment};
+  };
+  float m[2] = {__int_as_float(0xff800000), __int_as_float(0xff800000)}, l[2] = {}, acc[4] = {};
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float2 x = at(i).m(nt, c);
+    m[0] = fmaxf(m[0], x.x);
+    m[1] = fmaxf(m[1], x.y);
+  }
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const Fragment<C> f = at(i);
+    const float2 mi = f.m(nt, c), li = f.l(nt, c);
+    const float4 v = f.acc(q, lane);
+    const float e0 = join_factor(mi.x, m[0]), e1 = join_factor(mi.y, m[1]);
+    l[0] += li.x * e0;
+    l[1] += li.y * e1;
+    acc[0] += v.x * e0;
+    acc[1] += v.y * e1;
+    acc[2] += v.z * e0;
+    acc[3] += v.w * e1;
+  }
+  if (to) {
+    store_fragment<C>(to, q, lane, acc, m, l);
+  } else {
+    store_quad<C>(a, row, head, q, lane, acc, l);
+    if (q % (C::D / 16) == 0) store_lse(a, row, head, nt, lane, m, l);
+  }
+}
+
+// Four query elements at q[at ..], of either type and any alignment.
+static __device__ __noinline__ float4 load_query_slow(const void* q, int64_t at, int dtype) {
+  return make_float4(load_any(q, at, dtype), load_any(q, at + 1, dtype), load_any(q, at + 2, dtype),
+                     load_any(q, at + 3, dtype));
+}
+
+// The new token's K (kv = 0) or V row of a kv head, to its page.
+template <typename T, int D>
+__device__ __noinline__ void store_new_row(const PagedArgs& a, int32_t row, int32_t head, int64_t page,
+                                           int32_t in, int kv) {
+  const PageView& pv = a.pages;
+  const TokenView& s = kv ? a.vn : a.kn;
+  T* d = reinterpret_cast<T*>(kv ? pv.v : pv.k) + page * pv.stride_page + head * pv.stride_head + int64_t(in) * D;
+  float* sc = (kv ? pv.vs : pv.ks) + page * pv.sstride_page + head * pv.sstride_head + in;
+  store_token_row<T, D>(s.p, row * s.sb + head * s.sh, a.new_dtype, a.new_vec >> kv & 1, d, sc,
+                        int(threadIdx.x & 31));
+}
+
+template <typename T, int D, int NT, int QL, int PL>
+__global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
     paged_attention_kernel(const __grid_constant__ PagedArgs a) {
-  using C = PagedCfg<T, D, NT>;
+  using C = PagedCfg<T, D, NT, QL, PL>;
   constexpr int U = C::U, KW = C::KW, VW = C::VW, CH = C::CH, MT = D / 16;
   constexpr int KB = C::KL * C::ES, VB = C::VL * C::ES;  // bytes per load
+  constexpr int kRow = D * C::ES;                        // bytes of a token's row
+  constexpr float kNone = -__builtin_huge_valf();
   extern __shared__ __align__(16) char smem[];
   __shared__ Piece pieces[C::WARPS * 2];
   __shared__ int n_pieces[C::WARPS];
+  __shared__ int ids[C::WARPS];
   __shared__ int last_of[2];
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31), r = lane >> 2, c = lane & 3;
   char* fragments = smem;  // two per warp
-  uint4* qs = reinterpret_cast<uint4*>(smem + C::WARPS * 2 * C::kFragment + warp * C::q_bytes(a.q_limbs));
+  uint4* qs = reinterpret_cast<uint4*>(smem + C::WARPS * 2 * C::kFragment + warp * C::kQuery);
   const PageView& pv = a.pages;
   const int H = pv.H;
 
   // ---- the warp's share of the line of tiles
   const int per = (pv.n_rows + 31) / 32;
   int64_t mine = 0;
+#pragma unroll 1
   for (int i = 0; i < per; ++i) {
     const int b = lane * per + i;
-    if (b < pv.n_rows) mine += RowTiles(pv.batch[b].slot, pv.batch[b].len, a.window, a.sinks).n;
+    if (b < pv.n_rows) mine += RowTiles(pv.batch[b], a.window, a.sinks).n;
   }
   mine *= H;
   int64_t before = mine;  // inclusive, then exclusive prefix
@@ -345,13 +377,15 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
   }
   const int64_t total = __shfl_sync(0xffffffffu, before, 31);
   before -= mine;
-  // no fewer than U tiles per warp: a small batch takes fewer CTAs
-  int64_t ctas = (total + C::WARPS * U - 1) / (C::WARPS * U);
-  if (ctas > int64_t(gridDim.x)) ctas = gridDim.x;
-  if (int64_t(blockIdx.x) >= ctas) return;
-  const int64_t cta_from = total * blockIdx.x / ctas, cta_to = total * (blockIdx.x + 1) / ctas;
-  const int64_t from = cta_from + (cta_to - cta_from) * warp / C::WARPS;
-  const int64_t to = cta_from + (cta_to - cta_from) * (warp + 1) / C::WARPS;
+  // `chunk` tiles per warp, no fewer than U: a small batch takes fewer CTAs
+  constexpr uint32_t kFew = C::WARPS * U;
+  const uint32_t ctas = total >= int64_t(gridDim.x) * kFew ? gridDim.x : (uint32_t(total) + kFew - 1) / kFew;
+  const uint32_t workers = ctas * C::WARPS;
+  const int64_t chunk = total >> 31 ? (total + workers - 1) / workers : (uint32_t(total) + workers - 1) / workers;
+  const int64_t cta_chunk = chunk * C::WARPS, cta_from = cta_chunk * blockIdx.x;
+  if (cta_from >= total) return;
+  const int64_t cta_to = cta_from + cta_chunk < total ? cta_from + cta_chunk : total;
+  const int64_t from = cta_from + chunk * warp, to = from + chunk < cta_to ? from + chunk : cta_to;
 
   int32_t row = 0, head = 0, tile = 0;
   if (from < to) {
@@ -360,11 +394,13 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
     if (lane == src) {
       int64_t base = before;
       row = lane * per;
+#pragma unroll 1
       while (row < pv.n_rows) {
-        const int32_t n = RowTiles(pv.batch[row].slot, pv.batch[row].len, a.window, a.sinks).n;
+        const int32_t n = RowTiles(pv.batch[row], a.window, a.sinks).n;
         if (from < base + int64_t(n) * H) {
-          head = int32_t((from - base) / n);
-          tile = int32_t((from - base) % n);
+          const int64_t x = from - base;
+          head = x >> 31 ? int32_t(x / n) : int32_t(uint32_t(x) / uint32_t(n));
+          tile = int32_t(x - int64_t(head) * n);
           break;
         }
         base += int64_t(n) * H;
@@ -379,10 +415,33 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
   // ---- the segments of the share
   int made = 0;  // fragments left in shared memory
   int64_t at = from;
+#pragma unroll 1
   while (at < to && row < pv.n_rows) {
     const BatchRow br = pv.batch[row];
-    const RowTiles rt(br.slot, br.len, a.window, a.sinks);
+    const RowTiles rt(br, a.window, a.sinks);
     const int32_t end = int64_t(rt.n - tile) < to - at ? rt.n : tile + int32_t(to - at);
+    const int32_t Pm = (1 << pv.log2P) - 1;
+
+    // The table ahead of its use: lane j holds the pages of tile held + j (-1:
+    // nothing to read; a page of 8 tokens holds half a tile), and of the 32
+    // tiles after them; a bit per tile: all its tokens are seen.
+    struct Ahead {
+      int32_t page[2];
+      uint32_t full;
+    } cur, nxt;
+    int32_t held = tile;
+    auto fetch = [&](int32_t i, Ahead& g) {
+      g.page[0] = g.page[1] = -1;  // past the end: the last loads ahead read nothing
+      g.full = 0;
+      if (i >= end) return;
+      const int32_t t = rt.start(i + lane);
+      bool all = t + kTile <= rt.len && (t >= rt.lo || t + kTile <= rt.sinks);
+      g.page[0] = i + lane < end && t < rt.len ? page_of(pv, br.slot, t) : -1;
+      g.page[1] = g.page[0];
+      if (pv.log2P == 3) g.page[1] = i + lane < end && t + 8 < rt.len ? page_of(pv, br.slot, t + 8) : -1;
+      g.full = __ballot_sync(0xffffffffu, all && (g.page[0] | g.page[1]) >= 0);
+    };
+    fetch(held, cur);
 
     // query fragments, pre-split into limbs, to this warp's shared memory
     __syncwarp();
@@ -391,6 +450,16 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
     for (int nt = 0; nt < NT; ++nt) {
       const int g = nt * 8 + r;
       const int64_t qh = row * a.q.sb + (int64_t(head) * a.G + g) * a.q.sh;
+      if (C::ES == 2 && QL == 1 && (a.q_vec & 2)) {  // eight bf16 as they are
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (g < a.G)
+            w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + qh + i * 32 + c * 8));
+          qs[(nt * (D / 32) + i) * 32 + lane] = w;
+        }
+        continue;
+      }
       float x[D / 32][8];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
@@ -400,12 +469,12 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
           float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           if (g < a.G) {
             if (!a.q_vec) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = load_any(a.q.p, qh + d + e, a.q_dtype);
-            } else if (a.q_dtype == FC_DTYPE_F32) {
-              load_vec<float, 4>(static_cast<const float*>(a.q.p) + qh + d, y);
-            } else {
+              const float4 z = load_query_slow(a.q.p, qh + d, a.q_dtype);
+              y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
+            } else if (QL == 1 || a.q_dtype != FC_DTYPE_F32) {
               load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16*>(a.q.p) + qh + d, y);
+            } else {
+              load_vec<float, 4>(static_cast<const float*>(a.q.p) + qh + d, y);
             }
           }
 #pragma unroll
@@ -420,7 +489,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
           for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // (0 and NaN rows, and infinities: any scale will do)
+        // (a zero row or one with an infinity: any scale will do)
         int e = top > 0.0f && top <= 3.402823466e+38f ? exponent_of(top) : 14;
         e = e < -100 ? -100 : e;
         const float up = pow2i(14 - e);
@@ -432,7 +501,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
         qf[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c) * a.scale_log2e;
         qf[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4) * a.scale_log2e;
       }
-      for (int limb = 0; limb < a.q_limbs; ++limb)
+#pragma unroll
+      for (int limb = 0; limb < QL; ++limb)
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           uint32_t w[4];
@@ -444,67 +514,61 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
           qs[((limb * NT + nt) * (D / 32) + i) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    const char* kh = pv.k + int64_t(head) * pv.stride_head * C::ES;
-    const char* vh = pv.v + int64_t(head) * pv.stride_head * C::ES;
     if (a.kn.p && br.count > 0 && end == rt.n && rt.len > 0) {
       // the fused append: the warp with the segment's last tile stores the new
       // token's rows, which no other warp reads
-      const int32_t pos = rt.len - 1, pg = page_of(pv, br.slot, pos);
-      if (pg >= 0) {
-        const int32_t in = pos & ((1 << pv.log2P) - 1);
-        const int64_t e = pg * pv.stride_page + int64_t(in) * D;
-        const int64_t se = pg * pv.sstride_page + head * pv.sstride_head + in;
-        store_token_row<T, D>(a.kn.p, row * a.kn.sb + head * a.kn.sh, a.new_dtype, a.new_vec & 1,
-                              reinterpret_cast<T*>(const_cast<char*>(kh)) + e, pv.ks + se, lane);
-        store_token_row<T, D>(a.vn.p, row * a.vn.sb + head * a.vn.sh, a.new_dtype, a.new_vec & 2,
-                              reinterpret_cast<T*>(const_cast<char*>(vh)) + e, pv.vs + se, lane);
+      const int32_t page = page_of(pv, br.slot, rt.len - 1);
+      if (page >= 0) {
+        store_new_row<T, D>(a, row, head, page, (rt.len - 1) & Pm, 0);
+        store_new_row<T, D>(a, row, head, page, (rt.len - 1) & Pm, 1);
       }
     }
     __syncwarp();  // the query's fragments and the new token's rows are visible
+    fetch(held + 32, nxt);
 
-    float acc[C::NQ][4];
+    float acc[C::NQ][4] = {};
     float m[NT][2], l[NT][2];
 #pragma unroll
-    for (int q = 0; q < C::NQ; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.0f;
-#pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = __int_as_float(0xff800000);
+      m[nt][0] = m[nt][1] = kNone;
       l[nt][0] = l[nt][1] = 0.0f;
     }
-    int ve = 0;                                       // int8: see below
+    int ve = 0;  // int8: see below
     float v_most = -1.0f, v_mul = 0.0f, svc[U][2];
 
     uint32_t kr[U][2][KW / CH] = {}, vr[U][4][VW / CH] = {};
-    int32_t pg[U][2];                 // pages of the tiles' two halves
+    // where the tiles' halves are: bytes into the layer's pool, scales
+    int64_t off[U][2], soff[U][2];
+    const int64_t page_bytes = pv.stride_page * C::ES;
     float sk[U][2] = {}, sv[U][2] = {};  // int8: scales of tokens r and r + 8
-    bool full;                        // every token of the iteration is seen
+    bool full = false;                   // every token of the iteration is seen
+    // this lane's K row r and V row 2c within a half
+    const char* const kp = pv.k + head * (pv.stride_head * C::ES) + r * kRow + c * KB;
+    const char* const vp = pv.v + head * (pv.stride_head * C::ES) + 2 * c * kRow + r * VB;
 
-    const int32_t Pm = (1 << pv.log2P) - 1;
-    // The table ahead of its use: lane j holds the pages of tiles `held` + j
-    // (a page of 8 tokens holds half a tile) and of the 32 tiles after them.
-    int32_t held = tile, cur[2], nxt[2];
-    auto fetch = [&](int32_t i, int32_t (&g)[2]) {
-      const int32_t t = rt.start(i + lane);
-      const bool in = i + lane < end && t < rt.len;
-      g[0] = in ? page_of(pv, br.slot, t) : -1;
-      g[1] = pv.log2P > 3 ? g[0] : in && t + 8 < rt.len ? page_of(pv, br.slot, t + 8) : -1;
-    };
-    fetch(held, cur);
-    fetch(held + 32, nxt);
-    auto pages_of = [&](int32_t i) {
+    auto advance = [&](int32_t i) {  // to the tiles from i on
       if (i - held == 32) {
         held = i;
-        cur[0] = nxt[0];
-        cur[1] = nxt[1];
+        cur = nxt;
         fetch(held + 32, nxt);
       }
-      full = true;
+      const int j = i - held;
+      constexpr uint32_t kAll = (1u << U) - 1;
+      full = (cur.full >> j & kAll) == kAll;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        pg[u][0] = __shfl_sync(0xffffffffu, cur[0], i - held + u);
-        pg[u][1] = __shfl_sync(0xffffffffu, cur[1], i - held + u);
-        const int32_t t = rt.start(i + u);
-        full &= pg[u][0] >= 0 && pg[u][1] >= 0 && t + kTile <= rt.len && (t >= rt.lo || t + kTile <= rt.sinks);
+        const int32_t in = rt.start(i + u) & Pm;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int32_t x = hh == 0 || pv.log2P == 3 ? __shfl_sync(0xffffffffu, cur.page[hh], j + u) : -1;
+          if (hh == 0 || pv.log2P == 3) {
+            off[u][hh] = x < 0 ? -1 : x * page_bytes + ((in + 8 * hh) & Pm) * kRow;
+            if constexpr (C::ES == 1) soff[u][hh] = x * pv.sstride_page + ((in + 8 * hh) & Pm);
+          } else {
+            off[u][1] = off[u][0] < 0 ? -1 : off[u][0] + 8 * kRow;
+            if constexpr (C::ES == 1) soff[u][1] = soff[u][0] + 8;
+          }
+        }
       }
     };
     auto load_k = [&](int32_t i, int part) {
@@ -512,18 +576,23 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const int32_t t = rt.start(i + u) + hh * 8 + r;
-          const char* p = kh + (pg[u][hh] * pv.stride_page + int64_t(t & Pm) * D) * C::ES + c * KB;
-          if (full || (pg[u][hh] >= 0 && rt.sees(t))) {
+          const char* p = kp + off[u][hh] + part * (KW / CH) * 16;
+          if (full || (off[u][hh] >= 0 && rt.sees(rt.start(i + u) + hh * 8 + r))) {
 #pragma unroll
-            for (int j = 0; j < KW / CH; j += KB / 4)
-              load_words<KB>(&kr[u][hh][j], p + (j * 4 + part * (KW / CH) * 4) * 4);
-            if constexpr (C::ES == 1) {
-              const int64_t se = pg[u][hh] * pv.sstride_page + head * pv.sstride_head + (t & Pm);
-              load_words<4>(reinterpret_cast<uint32_t*>(&sk[u][hh]), pv.ks + se);
-              load_words<4>(reinterpret_cast<uint32_t*>(&sv[u][hh]), pv.vs + se);
-            }
-          } else if constexpr (C::ES == 1) {
+            for (int j = 0; j < KW / CH; j += KB / 4) load_words<KB>(&kr[u][hh][j], p + j * 16);
+          }
+        }
+    };
+    auto load_scales = [&](int32_t i) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int64_t se = soff[u][hh] + head * pv.sstride_head + r;
+          if (full || (off[u][hh] >= 0 && rt.sees(rt.start(i + u) + hh * 8 + r))) {
+            load_words<4>(reinterpret_cast<uint32_t*>(&sk[u][hh]), pv.ks + se);
+            load_words<4>(reinterpret_cast<uint32_t*>(&sv[u][hh]), pv.vs + se);
+          } else {
             sv[u][hh] = 0.0f;  // (a masked K row may hold anything: its score is replaced)
           }
         }
@@ -533,12 +602,10 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int32_t g = pg[u][k >> 1], t = rt.start(i + u) + (k >> 1) * 8 + 2 * c + (k & 1);
-          const char* p = vh + (g * pv.stride_page + int64_t(t & Pm) * D) * C::ES + r * VB;
-          if (full || (g >= 0 && rt.sees(t))) {
+          const char* p = vp + off[u][k >> 1] + (k & 1) * kRow + part * (VW / CH) * 32;
+          if (full || (off[u][k >> 1] >= 0 && rt.sees(rt.start(i + u) + (k >> 1) * 8 + 2 * c + (k & 1)))) {
 #pragma unroll
-            for (int j = 0; j < VW / CH; j += VB / 4)
-              load_words<VB>(&vr[u][k][j], p + (j * 8 + part * (VW / CH) * 8) * 4);
+            for (int j = 0; j < VW / CH; j += VB / 4) load_words<VB>(&vr[u][k][j], p + j * 32);
           } else {
 #pragma unroll
             for (int j = 0; j < VW / CH; ++j) vr[u][k][j] = 0;
@@ -546,275 +613,240 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
         }
     };
 
-    pages_of(tile);
-    if constexpr (C::kPrefetch) {
-      load_k(tile, 0);
-      load_v(tile, 0);
-    }
-    for (int32_t i = tile; i < end; i += U) {
-      // ---- S^T = K Q^T
+    // The first pass only loads (the loads' code is there once).
+#pragma unroll 1
+    for (int32_t i = C::kPrefetch ? tile - U : tile; i < end; i += U) {
+      const bool work = !C::kPrefetch || i >= tile;
       float s[U][NT][4];
+      if constexpr (!C::kPrefetch) {
+        advance(i);
+        if constexpr (C::ES == 1) load_scales(i);
+      }
+      if (work) {
+        // ---- S^T = K Q^T
+        float odd[U][NT][4];  // a second chain of dependent products
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.0f;
-#pragma unroll
-      for (int part = 0; part < CH; ++part) {
-        if constexpr (!C::kPrefetch) load_k(i, part);
-        constexpr int STEPS = D / 16 / CH;  // k-steps of 16 channels per part
-        if constexpr (C::ES == 4) {
-#pragma unroll
-          for (int ks = 0; ks < STEPS; ++ks)
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              float x[2][4];
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[hh][e] = __uint_as_float(kr[u][hh][4 * ks + e]);
-#pragma unroll
-              for (int kl = 0; kl < 3; ++kl) {
-                const uint32_t a0 = take_limb(x[0][0], x[0][1]), a2 = take_limb(x[0][2], x[0][3]);
-                const uint32_t a1 = take_limb(x[1][0], x[1][1]), a3 = take_limb(x[1][2], x[1][3]);
-#pragma unroll
-                for (int ql = 0; ql < 3 - kl; ++ql) {
-                  if (ql >= a.q_limbs) break;
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    const int kk = part * STEPS + ks;
-                    const uint2 b = reinterpret_cast<const uint2*>(
-                        &qs[((ql * NT + nt) * (D / 32) + kk / 2) * 32 + lane])[kk & 1];
-                    mma_bf16(s[u][nt], a0, a1, a2, a3, b.x, b.y);
-                  }
-                }
-              }
-            }
-        } else {
-          // bf16, int8: K is exact in one limb; the limbs of the query
-          float odd[U][NT][4] = {};  // a second chain of dependent products
+        for (int part = 0; part < CH; ++part) {
+          if constexpr (!C::kPrefetch) load_k(i, part);
+          constexpr int STEPS = D / 16 / CH;  // k-steps of 16 channels per part
+          static_assert(STEPS % 2 == 0, "two chains");
 #pragma unroll
           for (int ks = 0; ks < STEPS; ++ks) {
             const int kk = part * STEPS + ks;
-            uint32_t k0[U], k1[U], k2[U], k3[U];
+            // fp32 pages have three limbs; the others are exact as they are
+            constexpr int KLIMBS = C::ES == 4 ? 3 : 1;
+            uint32_t ka[U][KLIMBS][4];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-              if constexpr (C::ES == 2) {
-                k0[u] = kr[u][0][2 * ks];
-                k1[u] = kr[u][1][2 * ks];
-                k2[u] = kr[u][0][2 * ks + 1];
-                k3[u] = kr[u][1][2 * ks + 1];
+              if constexpr (C::ES == 4) {
+                float x[2][4];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) x[hh][e] = __uint_as_float(kr[u][hh][4 * ks + e]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) ka[u][k][e] = take_limb(x[e & 1][e & 2], x[e & 1][(e & 2) + 1]);
+              } else if constexpr (C::ES == 2) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ka[u][0][e] = kr[u][e & 1][2 * ks + (e >> 1)];
               } else {
-                const uint32_t x0 = kr[u][0][ks] ^ 0x80808080u, x1 = kr[u][1][ks] ^ 0x80808080u;
-                k0[u] = codes_to_f16(__byte_perm(x0, 0x64646464u, 0x4140));
-                k1[u] = codes_to_f16(__byte_perm(x1, 0x64646464u, 0x4140));
-                k2[u] = codes_to_f16(__byte_perm(x0, 0x64646464u, 0x4342));
-                k3[u] = codes_to_f16(__byte_perm(x1, 0x64646464u, 0x4342));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  ka[u][0][e] = codes_to_f16(
+                      __byte_perm(kr[u][e & 1][ks] ^ 0x80808080u, 0x64646464u, e < 2 ? 0x4140 : 0x4342));
               }
             }
 #pragma unroll
-            for (int ql = 0; ql < (C::ES == 1 ? 2 : 3); ++ql) {
-              if (ql >= a.q_limbs) break;
+            for (int ql = 0; ql < QL; ++ql)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 const uint2 b = reinterpret_cast<const uint2*>(
                     &qs[((ql * NT + nt) * (D / 32) + kk / 2) * 32 + lane])[kk & 1];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                  if (ks & 1) mma<T>(odd[u][nt], k0[u], k1[u], k2[u], k3[u], b.x, b.y);
-                  else mma<T>(s[u][nt], k0[u], k1[u], k2[u], k3[u], b.x, b.y);
-                }
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                  for (int k = 0; k < KLIMBS; ++k) {
+                    if (k + ql > 2) continue;
+                    auto& d = kk & 1 ? odd[u][nt] : s[u][nt];
+                    if (kk < 2 && ql == 0 && k == 0) mma<T, true>(d, ka[u][k], b.x, b.y);
+                    else mma<T, false>(d, ka[u][k], b.x, b.y);
+                  }
               }
-            }
           }
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s[u][nt][e] += odd[u][nt][e];
         }
-      }
-
-      // ---- scores in the log2 domain, masked
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if constexpr (C::ES == 1) s[u][nt][2 * hh + j] *= sk[u][hh] * qf[nt][j];
-              else s[u][nt][2 * hh + j] *= a.scale_log2e;
-            }
-      if (!full) {
+        // ---- scores in the log2 domain, masked
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            if (pg[u][hh] >= 0 && rt.sees(rt.start(i + u) + hh * 8 + r)) continue;
+          for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              s[u][nt][2 * hh] = s[u][nt][2 * hh + 1] = __int_as_float(0xff800000);
-          }
-      }
-      if constexpr (C::ES == 1) {
-        // V's scales are multiplied into P as 2^(7 - ve) scale, ve above the
-        // exponent of every scale so far, so that fp16 holds them (p <= 2^8)
-        float x = 0.0f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) x = fmaxf(x, fmaxf(sv[u][0], sv[u][1]));
-        if (__any_sync(0xffffffffu, x > v_most)) {
-          x = warp_max(x);
-          int e = exponent_of(x) + 1;
-          e = e < -100 ? -100 : e > 120 ? 120 : e;
-          const float f = v_most < 0.0f ? 0.0f : pow2i(ve - e < -126 ? -126 : ve - e);
-          ve = e;
-          v_most = pow2i(e);
-          v_mul = pow2i(7 - e);
+              for (int j = 0; j < 2; ++j) {
+                float& x = s[u][nt][2 * hh + j];
+                x += odd[u][nt][2 * hh + j];
+                if constexpr (C::ES == 1) x *= sk[u][hh] * qf[nt][j];
+                else x *= a.scale_log2e;
+              }
+        if (!full) {
 #pragma unroll
-          for (int q = 0; q < C::NQ; ++q)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[q][k] *= f;
+            for (int hh = 0; hh < 2; ++hh) {
+              if (off[u][hh] >= 0 && rt.sees(rt.start(i + u) + hh * 8 + r)) continue;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) s[u][nt][2 * hh] = s[u][nt][2 * hh + 1] = kNone;
+            }
         }
+        if constexpr (C::ES == 1) {
+          // V's scales are multiplied into P as 2^(7 - ve) scale, ve above the
+          // exponent of every scale so far, so that fp16 holds them (p <= 2^8)
+          float x = 0.0f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          svc[u][0] = sv[u][0] * v_mul;  // before the prefetch
-          svc[u][1] = sv[u][1] * v_mul;
+          for (int u = 0; u < U; ++u) x = fmaxf(x, fmaxf(sv[u][0], sv[u][1]));
+          if (__any_sync(0xffffffffu, x > v_most)) {
+            x = warp_max(x);
+            int e = exponent_of(x) + 1;
+            e = e < -100 ? -100 : e > 120 ? 120 : e;
+            const float f = v_most < 0.0f ? 0.0f : pow2i(ve - e < -126 ? -126 : ve - e);
+            ve = e;
+            v_most = pow2i(e);
+            v_mul = pow2i(7 - e);
+#pragma unroll
+            for (int q = 0; q < C::NQ; ++q)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[q][k] *= f;
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            svc[u][0] = sv[u][0] * v_mul;  // before the next ones are loaded
+            svc[u][1] = sv[u][1] * v_mul;
+          }
         }
       }
       if constexpr (C::kPrefetch) {
-        pages_of(i + U);
+        advance(i + U);
         load_k(i + U, 0);
+        if constexpr (C::ES == 1) load_scales(i + U);
       }
-
-      // ---- running maximum, raised only where a score passes it by 2^kLazy
-      bool raise = false;
-      float top[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x = fmaxf(s[0][nt][j], s[0][nt][2 + j]);
-#pragma unroll
-          for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(s[u][nt][j], s[u][nt][2 + j]));
-          top[nt][j] = x;
-          raise |= x > m[nt][j] + kLazy;
-        }
-      if (__any_sync(0xffffffffu, raise)) {
+      if (work) {
+        // ---- running maximum, raised only where a score passes it by 2^kLazy
+        bool raise = false;
+        float top[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float x = top[nt][j];
+            float x = fmaxf(s[0][nt][j], s[0][nt][2 + j]);
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            x = fmaxf(x, m[nt][j]);
-            const float e = join_factor(m[nt][j], x);
-            m[nt][j] = x;
-            l[nt][j] *= e;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              acc[nt * MT + mt][j] *= e;
-              acc[nt * MT + mt][2 + j] *= e;
-            }
+            for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(s[u][nt][j], s[u][nt][2 + j]));
+            top[nt][j] = x;
+            raise |= x > m[nt][j] + kLazy;
           }
-      }
-
-      // ---- P, and its limbs as B operands (heads x tokens)
-      uint32_t pb[U][3][NT][2];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float p[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              // no score yet: the maximum is -infinity and p is to be 0
-              const float base = m[nt][j] == __int_as_float(0xff800000) ? 0.0f : m[nt][j];
-              p[j] = fast_exp2(s[u][nt][2 * hh + j] - base);
-              l[nt][j] += p[j];
-              if constexpr (C::ES == 1) p[j] *= svc[u][hh];
-            }
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              if constexpr (C::ES == 1) {
-                if (k < 2) pb[u][k][nt][hh] = transpose8x8(take_limb_f16(p[0], p[1]));
-                continue;
-              }
-              // the last limb is rounded, the ones before keep eight bits each
-              if (k < a.p_limbs - 1) pb[u][k][nt][hh] = transpose8x8(take_limb(p[0], p[1]));
-              else if (k < a.p_limbs) pb[u][k][nt][hh] = transpose8x8(pack_bf16(p[0], p[1]));
-            }
-          }
-
-      // ---- O^T += V^T P^T: the iteration's products in accumulators of their
-      // own, added in fp32 (the tensor cores' running sums are truncated)
-#pragma unroll
-      for (int part = 0; part < CH; ++part) {
-        if constexpr (!C::kPrefetch) load_v(i, part);
-#pragma unroll
-        for (int mt = 0; mt < MT / CH; ++mt) {
-          const int q = part * (MT / CH) + mt;
-          float o[NT][4] = {};
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if constexpr (C::ES == 4) {
-              float x[4][2];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) x[k][e] = __uint_as_float(vr[u][k][2 * mt + e]);
-#pragma unroll
-              for (int vl = 0; vl < 3; ++vl) {
-                const uint32_t a0 = take_limb(x[0][0], x[1][0]), a1 = take_limb(x[0][1], x[1][1]);
-                const uint32_t a2 = take_limb(x[2][0], x[3][0]), a3 = take_limb(x[2][1], x[3][1]);
-#pragma unroll
-                for (int k = 0; k < 3 - vl; ++k)
-                  if (k < a.p_limbs) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                      mma_bf16(o[nt], a0, a1, a2, a3, pb[u][k][nt][0], pb[u][k][nt][1]);
-                  }
-              }
-            } else {
-              uint32_t a0, a1, a2, a3;
-              if constexpr (C::ES == 2) {
-                a0 = __byte_perm(vr[u][0][mt], vr[u][1][mt], 0x5410);
-                a1 = __byte_perm(vr[u][0][mt], vr[u][1][mt], 0x7632);
-                a2 = __byte_perm(vr[u][2][mt], vr[u][3][mt], 0x5410);
-                a3 = __byte_perm(vr[u][2][mt], vr[u][3][mt], 0x7632);
-              } else {
-                // codes 2 mt and 2 mt + 1 of each token: bytes of word mt / 2
-                const uint32_t lo = mt & 1 ? 0x0602u : 0x0400u, hi = mt & 1 ? 0x0703u : 0x0501u;
-                auto pair = [](uint32_t w0, uint32_t w1, uint32_t sel) {
-                  return codes_to_f16((__byte_perm(w0, w1, sel) & 0x00ff00ffu) ^ 0x64806480u);
-                };
-                a0 = pair(vr[u][0][mt / 2], vr[u][1][mt / 2], lo);
-                a1 = pair(vr[u][0][mt / 2], vr[u][1][mt / 2], hi);
-                a2 = pair(vr[u][2][mt / 2], vr[u][3][mt / 2], lo);
-                a3 = pair(vr[u][2][mt / 2], vr[u][3][mt / 2], hi);
-              }
-              constexpr int kMost = C::ES == 1 ? 2 : 3;
-#pragma unroll
-              for (int k = 0; k < kMost; ++k)
-                if (C::ES == 1 || k < a.p_limbs) {
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
-                    mma<T>(o[nt], a0, a1, a2, a3, pb[u][k][nt][0], pb[u][k][nt][1]);
-                }
-            }
-          }
+        if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt * MT + q][e] += o[nt][e];
+            for (int j = 0; j < 2; ++j) {
+              float x = top[nt][j];
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+              x = fmaxf(x, m[nt][j]);
+              const float e = join_factor(m[nt][j], x);
+              m[nt][j] = x;
+              l[nt][j] *= e;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                acc[nt * MT + mt][j] *= e;
+                acc[nt * MT + mt][2 + j] *= e;
+              }
+            }
+        }
+
+        // ---- P, and its limbs as B operands (heads x tokens)
+        uint32_t pb[U][PL][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          // no score yet: the maximum is -infinity and p is to be 0
+          const float b0 = m[nt][0] == kNone ? 0.0f : m[nt][0], b1 = m[nt][1] == kNone ? 0.0f : m[nt][1];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              float p0 = fast_exp2(s[u][nt][2 * hh] - b0), p1 = fast_exp2(s[u][nt][2 * hh + 1] - b1);
+              l[nt][0] += p0;
+              l[nt][1] += p1;
+              if constexpr (C::ES == 1) {
+                p0 *= svc[u][hh];
+                p1 *= svc[u][hh];
+              }
+#pragma unroll
+              for (int k = 0; k < PL; ++k) {
+                // bf16: the last limb is rounded, the ones before are cut at eight bits
+                const uint32_t w = C::ES == 1 ? take_limb_f16(p0, p1)
+                                              : k == PL - 1 ? pack_bf16(p0, p1) : take_limb(p0, p1);
+                pb[u][k][nt][hh] = transpose8x8(w);
+              }
+            }
+        }
+
+        // ---- O^T += V^T P^T: the iteration's products in accumulators of their
+        // own, added in fp32 (the tensor cores' running sums are truncated)
+#pragma unroll
+        for (int part = 0; part < CH; ++part) {
+          if constexpr (!C::kPrefetch) load_v(i, part);
+#pragma unroll
+          for (int mt = 0; mt < MT / CH; ++mt) {
+            float o[NT][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              constexpr int VLIMBS = C::ES == 4 ? 3 : 1;
+              uint32_t va[VLIMBS][4];
+              if constexpr (C::ES == 4) {
+                float x[4][2];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) x[k][e] = __uint_as_float(vr[u][k][2 * mt + e]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) va[k][e] = take_limb(x[e & 2][e & 1], x[(e & 2) + 1][e & 1]);
+              } else if constexpr (C::ES == 2) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  va[0][e] = __byte_perm(vr[u][e & 2][mt], vr[u][(e & 2) + 1][mt], e & 1 ? 0x7632 : 0x5410);
+              } else {
+                // codes 2 mt and 2 mt + 1 of each token: bytes of word mt / 2
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t sel = (mt & 1 ? 0x0602u : 0x0400u) + (e & 1 ? 0x0101u : 0u);
+                  va[0][e] = codes_to_f16(
+                      (__byte_perm(vr[u][e & 2][mt / 2], vr[u][(e & 2) + 1][mt / 2], sel) & 0x00ff00ffu) ^ 0x64806480u);
+                }
+              }
+#pragma unroll
+              for (int v = 0; v < VLIMBS; ++v)
+#pragma unroll
+                for (int k = 0; k < PL; ++k) {
+                  if (v + k > 2) continue;
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    if (u == 0 && v == 0 && k == 0) mma<T, true>(o[nt], va[v], pb[u][k][nt][0], pb[u][k][nt][1]);
+                    else mma<T, false>(o[nt], va[v], pb[u][k][nt][0], pb[u][k][nt][1]);
+                  }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[nt * MT + part * (MT / CH) + mt][e] += o[nt][e];
+          }
         }
       }
       if constexpr (C::kPrefetch) load_v(i + U, 0);
-      else pages_of(i + U);
     }
 
     // ---- the segment's sums over the lanes' tokens; whole segments are done
@@ -834,13 +866,12 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
     const bool whole = tile == 0 && end == rt.n;
     char* frag = fragments + (warp * 2 + made) * C::kFragment;
 #pragma unroll
-    for (int q = 0; q < C::NQ; ++q) {
-      if (whole) store_quad<C, T>(a, row, head, q, lane, acc[q], l[q / MT]);
-      else store_fragment<C>(frag, q, lane, acc[q], m[q / MT], l[q / MT]);
-    }
+    for (int q = 0; q < C::NQ; ++q) store_fragment<C>(frag, q, lane, acc[q], m[q / MT], l[q / MT]);
     if (whole) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) store_lse(a, row, head, nt, lane, m[nt], l[nt]);
+      __syncwarp();
+      const int mine_at = warp * 2 + made;
+#pragma unroll 1
+      for (int q = 0; q < C::NQ; ++q) join_quad<C>(a, fragments, nullptr, mine_at, 1, nullptr, row, head, q);
     } else {
       if (lane == 0) pieces[warp * 2 + made] = Piece{row, head, tile, end, rt.n};
       ++made;
@@ -853,66 +884,59 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
   __syncthreads();
 
   // ---- join the CTA's fragments, segment by segment, in order
-  int open = 0;                       // segments left to other CTAs as well
-  int32_t seg_row[2], seg_head[2], seg_n[2];
-  int64_t first_pos[2];               // line position of the segment's tile 0
-  {
-    // line position of the fragments: walk the CTA's range
-    int w = 0, k = 0;
+  int open = 0;                    // segments left to other CTAs as well
+  int32_t seg_row[2], seg_head[2];
+  int32_t cta0[2], cta1[2];        // the segment's first and last CTA
+#pragma unroll 1
+  for (int w = 0, k = 0; w < C::WARPS;) {
+    if (k >= n_pieces[w]) {
+      ++w;
+      k = 0;
+      continue;
+    }
+    const Piece first = pieces[w * 2 + k];
+    int n = 0;
+    int32_t upto = first.from;
+    // consecutive fragments of one segment: at most one per warp
+#pragma unroll 1
     while (w < C::WARPS) {
       if (k >= n_pieces[w]) {
         ++w;
         k = 0;
         continue;
       }
-      const Piece first = pieces[w * 2 + k];
-      int ids[C::WARPS], n = 0;
-      int32_t upto = first.from;
-      // consecutive fragments of one segment: at most one per warp
-      while (w < C::WARPS) {
-        if (k >= n_pieces[w]) {
-          ++w;
-          k = 0;
-          continue;
-        }
-        const Piece p = pieces[w * 2 + k];
-        if (p.row != first.row || p.head != first.head) break;
-        ids[n++] = w * 2 + k;
-        upto = p.to;
-        ++k;
-      }
-      const bool whole = first.from == 0 && upto == first.n;
-      char* to_ws = a.partials + (int64_t(blockIdx.x) * 2 + (first.from > 0 ? 0 : 1)) * C::kFragment;
-      for (int q = warp; q < C::NQ; q += C::WARPS) {
-        float o[4], mm[2], ll[2];
-        join<C>(n, [&](int i) { return fragments + ids[i] * C::kFragment; }, q, lane, o, mm, ll);
-        if (whole) {
-          store_quad<C, T>(a, first.row, first.head, q, lane, o, ll);
-          if (q % MT == 0) store_lse(a, first.row, first.head, q / MT, lane, mm, ll);
-        } else {
-          store_fragment<C>(to_ws, q, lane, o, mm, ll);
-        }
-      }
-      if (!whole) {
-        const int j = open++ & 1;
-        seg_row[j] = first.row;
-        seg_head[j] = first.head;
-        seg_n[j] = first.n;
-        // a segment that began before this CTA starts `from` tiles before its
-        // range; one that runs past its end begins upto - from tiles before it
-        first_pos[j] = first.from > 0 ? cta_from - first.from : cta_to - upto;
-      }
+      const Piece p = pieces[w * 2 + k];
+      if (p.row != first.row || p.head != first.head) break;
+      if (threadIdx.x == 0) ids[n] = w * 2 + k;
+      ++n;
+      upto = p.to;
+      ++k;
     }
+    __syncthreads();
+    const bool whole = first.from == 0 && upto == first.n;
+    char* to_ws = a.partials + (int64_t(blockIdx.x) * 2 + (first.from > 0 ? 0 : 1)) * C::kFragment;
+#pragma unroll 1
+    for (int q = warp; q < C::NQ; q += C::WARPS)
+      join_quad<C>(a, fragments, ids, 0, n, whole ? nullptr : to_ws, first.row, first.head, q);
+    if (!whole) {
+      const int j = open++ & 1;
+      seg_row[j] = first.row;
+      seg_head[j] = first.head;
+      // its tiles before and after this CTA's, in whole CTAs
+      const uint32_t span = cta_chunk >> 31 ? 0x7fffffffu : uint32_t(cta_chunk);
+      cta0[j] = int32_t(blockIdx.x - (uint32_t(first.from) + span - 1) / span);
+      cta1[j] = int32_t(blockIdx.x + (uint32_t(first.n - upto) + span - 1) / span);
+    }
+    __syncthreads();
   }
   if (open == 0) return;
 
   // ---- the last CTA of a segment joins the CTAs' fragments
   __threadfence();
   __syncthreads();
+#pragma unroll 1
   for (int j = 0; j < open; ++j) {
-    // the CTA of position p is the largest c with total c / ctas <= p
-    const int64_t p0 = first_pos[j], p1 = p0 + seg_n[j] - 1;
-    const int32_t c0 = int32_t(((p0 + 1) * ctas - 1) / total), c1 = int32_t(((p1 + 1) * ctas - 1) / total);
+    const int32_t c0 = cta0[j], c1 = cta1[j];
     if (threadIdx.x == 0) {
       const uint32_t n = atomicAdd(&a.tickets[c0], 1u);
       last_of[j] = n == uint32_t(c1 - c0);
@@ -921,49 +945,40 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT>::WARPS * 32, 1)
     __syncthreads();
     if (!last_of[j]) continue;
     __threadfence();
-    for (int q = warp; q < C::NQ; q += C::WARPS) {
-      float o[4], mm[2], ll[2];
-      join<C>(c1 - c0 + 1,
-              [&](int i) { return a.partials + (int64_t(c0 + i) * 2 + (i == 0 ? 1 : 0)) * C::kFragment; }, q,
-              lane, o, mm, ll);
-      store_quad<C, T>(a, seg_row[j], seg_head[j], q, lane, o, ll);
-      if (q % MT == 0) store_lse(a, seg_row[j], seg_head[j], q / MT, lane, mm, ll);
-    }
+#pragma unroll 1
+    for (int q = warp; q < C::NQ; q += C::WARPS)
+      join_quad<C>(a, a.partials, nullptr, 2 * c0 + 1, c1 - c0 + 1, nullptr, seg_row[j], seg_head[j], q);
   }
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, int QL, int PL>
 int launch_paged(const PagedArgs& a, cudaStream_t s) {
-  using C = PagedCfg<T, D, NT>;
-  const size_t smem = C::WARPS * (2 * C::kFragment + C::q_bytes(a.q_limbs));
-  auto* kernel = paged_attention_kernel<T, D, NT>;
-  // once per device: the attribute allows the largest form (three limbs)
-  static std::atomic<bool> set[64];
+  using C = PagedCfg<T, D, NT, QL, PL>;
+  auto* kernel = paged_attention_kernel<T, D, NT, QL, PL>;
+  static std::atomic<bool> set[64];  // once per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FC_ERR_CUDA;
   if (!set[dev]) {
-    const size_t most = C::WARPS * (2 * C::kFragment + C::q_bytes(3));
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most)) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kShared)) != cudaSuccess)
       return FC_ERR_CUDA;
     set[dev] = true;
   }
-  const unsigned grid = unsigned(sm_count() * kPagedCtasPerSm);
-  kernel<<<grid, C::WARPS * 32, smem, s>>>(a);
+  kernel<<<unsigned(sm_count() * kPagedCtasPerSm), C::WARPS * 32, C::kShared, s>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
-template <typename T>
-int launch_paged_dtype(const PagedArgs& a, int64_t D, cudaStream_t s) {
+template <typename T, int QL, int PL>
+int launch_paged_sizes(const PagedArgs& a, int64_t D, cudaStream_t s) {
   const bool two = a.G > 8;
   switch (D) {
     case 32:
-      return two ? launch_paged<T, 32, 2>(a, s) : launch_paged<T, 32, 1>(a, s);
+      return two ? launch_paged<T, 32, 2, QL, PL>(a, s) : launch_paged<T, 32, 1, QL, PL>(a, s);
     case 64:
-      return two ? launch_paged<T, 64, 2>(a, s) : launch_paged<T, 64, 1>(a, s);
+      return two ? launch_paged<T, 64, 2, QL, PL>(a, s) : launch_paged<T, 64, 1, QL, PL>(a, s);
     case 128:
-      return two ? launch_paged<T, 128, 2>(a, s) : launch_paged<T, 128, 1>(a, s);
+      return two ? launch_paged<T, 128, 2, QL, PL>(a, s) : launch_paged<T, 128, 1, QL, PL>(a, s);
     case 256:
-      return two ? launch_paged<T, 256, 2>(a, s) : launch_paged<T, 256, 1>(a, s);
+      return two ? launch_paged<T, 256, 2, QL, PL>(a, s) : launch_paged<T, 256, 1, QL, PL>(a, s);
   }
   return FC_ERR_UNSUPPORTED;
 }

@@ -169,6 +169,35 @@ def test_many_short_sequences():
     check_attention(f.cache.attention(q.to(DEV)), q, f, 1)
 
 
+@pytest.mark.parametrize("kv,n", [("f32", 512), ("i8", 1024), ("bf16", 496)])
+def test_shares_that_end_with_the_table_lookahead(kv, n):
+    """A warp takes the pages of 32 tiles (of 16 tokens) at a time; here every
+    sequence has exactly 32 or 64 tiles, or one less, and there are as many
+    sequences as the GPU has warps at work or a few more, so that shares end
+    where a lookahead does."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = 12 * sms + 5
+    gen = torch.Generator().manual_seed(10)
+    f = Filled([n] * 2, kv, Hk=1, D=32, seed=3)
+    own = f.cache
+    c = PagedKVCache(1, rows, own.n_pages, 1, 32, max_pages=own.max_pages,
+                     kv=kv, token_dtype=BF, device=DEV,
+                     storage=(own.k, own.v, own.k_scales, own.v_scales))
+    # the two sequences' pages, shared by all rows
+    table = own.save_map()[0].repeat(-(-rows // 2), 1)[:rows].contiguous()
+    c.restore_map(table, torch.full((rows,), n, dtype=torch.int32))
+    q = rand(gen, rows, 1, 1, 32, dtype=BF)
+    c.begin(range(rows), 0)
+    got = c.attention(q.to(DEV))
+    some = [0, 1, 2, rows // 2, rows - 2, rows - 1]
+    check_attention(got[some], q[some], f, 1, slots=[i % 2 for i in some])
+    for odd in (0, 1):      # equal queries give equal outputs in every row
+        qq = q[odd:odd + 1].expand(rows, 1, 1, 32).contiguous().to(DEV)
+        o = c.attention(qq)[odd::2]
+        err = (o - o[:1]).abs().max() / o.abs().max()
+        assert float(err) <= 2.0 ** -17     # splits differ by rounding only
+
+
 def test_strides_scale_and_alignment():
     """Queries and outputs at odd offsets and strides; what lies around the
     outputs stays."""
