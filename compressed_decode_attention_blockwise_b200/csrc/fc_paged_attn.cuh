@@ -205,8 +205,29 @@ struct RowTiles {
 // part is empty, or all its scores are NaN and have to stay so).
 __device__ __forceinline__ float join_factor(float m, float M) { return m == M ? 1.0f : fast_exp2(m - M); }
 
-// Writes the (already joined) accumulator quad q of one lane: heads 8 nt + 2c
-// and + 1, channels d and d + 1 of D.
+// Two neighbouring outputs.
+__device__ __forceinline__ void store_pair(const PagedArgs& a, int64_t at, float x0, float x1) {
+  if (a.out_dtype == FC_DTYPE_F32) {
+    float* o = static_cast<float*>(a.out) + at;
+    if (a.out_vec) {
+      *reinterpret_cast<float2*>(o) = make_float2(x0, x1);
+    } else {
+      o[0] = x0;
+      o[1] = x1;
+    }
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
+    if (a.out_vec) {
+      *reinterpret_cast<uint32_t*>(o) = pack_bf16(x0, x1);
+    } else {
+      o[0] = __float2bfloat16_rn(x0);
+      o[1] = __float2bfloat16_rn(x1);
+    }
+  }
+}
+
+// Writes the accumulator quad q of one lane: heads 8 nt + 2c and + 1, two
+// neighbouring channels of D.
 template <typename C>
 __device__ __forceinline__ void store_quad(const PagedArgs& a, int32_t row, int32_t head, int q, int lane,
                                            const float (&acc)[4], const float (&l)[2]) {
@@ -217,26 +238,35 @@ __device__ __forceinline__ void store_quad(const PagedArgs& a, int32_t row, int3
     const int g = nt * 8 + 2 * c + j;
     if (g >= a.G) continue;
     const float inv = l[j] == 0.0f ? 0.0f : 1.0f / l[j];
-    const float x0 = l[j] == 0.0f ? 0.0f : acc[j] * inv, x1 = l[j] == 0.0f ? 0.0f : acc[2 + j] * inv;
-    const int64_t at = row * a.os_b + (int64_t(head) * a.G + g) * a.os_h + d;
-    if (a.out_dtype == FC_DTYPE_F32) {
-      float* o = static_cast<float*>(a.out) + at;
-      if (a.out_vec) {
-        *reinterpret_cast<float2*>(o) = make_float2(x0, x1);
-      } else {
-        o[0] = x0;
-        o[1] = x1;
-      }
-    } else {
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
-      if (a.out_vec) {
-        *reinterpret_cast<uint32_t*>(o) = pack_bf16(x0, x1);
-      } else {
-        o[0] = __float2bfloat16_rn(x0);
-        o[1] = __float2bfloat16_rn(x1);
+    const bool none = l[j] == 0.0f;  // an empty row's zeros
+    store_pair(a, row * a.os_b + (int64_t(head) * a.G + g) * a.os_h + d, none ? 0.0f : acc[j] * inv,
+               none ? 0.0f : acc[2 + j] * inv);
+  }
+}
+
+// The same for all quads of a segment that one warp holds whole.
+template <typename C, typename TO>
+__device__ __forceinline__ void store_all(const PagedArgs& a, int32_t row, int32_t head, int lane,
+                                          const float (&acc)[C::NQ][4], const float (&l)[C::NT][2]) {
+  constexpr int MT = C::D / 16;
+  const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int g = nt * 8 + 2 * c + j;
+      if (g >= a.G) continue;
+      const float inv = l[nt][j] == 0.0f ? 0.0f : 1.0f / l[nt][j];
+      TO* o = static_cast<TO*>(a.out) + row * a.os_b + (int64_t(head) * a.G + g) * a.os_h + r * C::VL;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int idx = 2 * mt, d = idx / C::VL * 8 * C::VL + idx % C::VL;
+        // (an empty row's accumulators are zero)
+        const float x0 = acc[nt * MT + mt][j] * inv, x1 = acc[nt * MT + mt][2 + j] * inv;
+        if constexpr (sizeof(TO) == 4) *reinterpret_cast<float2*>(o + d) = make_float2(x0, x1);
+        else *reinterpret_cast<uint32_t*>(o + d) = pack_bf16(x0, x1);
       }
     }
-  }
 }
 
 // lse = ln 2 (m + log2 l) of the lane's two heads, by the lanes of row r = 0.
@@ -284,42 +314,76 @@ __device__ __forceinline__ void store_fragment(char* p, int q, int lane, const f
   }
 }
 
-// Joins n fragments for quad q and stores the result, as the row's output (to
-// null) or as a fragment. Fragment i lies at base + kFragment * ids[i], or, in
-// the workspace (ids null), at first, first + 1, first + 3, ...: the segment's
-// first CTA left its second fragment, every later one its first.
-template <typename C>
-__device__ __noinline__ void join_quad(const PagedArgs& a, const char* base, const int* ids, int first, int n,
-                                       char* to, int32_t row, int32_t head, int q) {
-  const int lane = int(threadIdx.x & 31), nt = q / (C::D / 16), c = lane & 3;
-  auto at = [&](int i) {
-    return Fragment<C>{base + size_t(ids ? ids[i] : i == 0 ? first : first + 2 * i - 1) * C::kFragment};
-  };
-  float m[2] = {__int_as_float(0xff800000), __int_as_float(0xff800000)}, l[2] = {}, acc[4] = {};
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float2 x = at(i).m(nt, c);
-    m[0] = fmaxf(m[0], x.x);
-    m[1] = fmaxf(m[1], x.y);
+// The running join of fragments: maxima, sums and one quad of accumulators.
+struct Joined {
+  float m[2], l[2], acc[4];
+  __device__ __forceinline__ Joined()
+      : m{-__builtin_huge_valf(), -__builtin_huge_valf()}, l{0.0f, 0.0f}, acc{0.0f, 0.0f, 0.0f, 0.0f} {}
+  // Takes N more fragments at once (the loads of all of them first).
+  template <int N>
+  __device__ __forceinline__ void take(const float2 (&mi)[N], const float2 (&li)[N], const float4 (&v)[N]) {
+    float x0 = m[0], x1 = m[1];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x0 = fmaxf(x0, mi[i].x);
+      x1 = fmaxf(x1, mi[i].y);
+    }
+    const float f0 = join_factor(m[0], x0), f1 = join_factor(m[1], x1);
+    m[0] = x0;
+    m[1] = x1;
+    l[0] *= f0;
+    l[1] *= f1;
+    acc[0] *= f0;
+    acc[1] *= f1;
+    acc[2] *= f0;
+    acc[3] *= f1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float e0 = join_factor(mi[i].x, x0), e1 = join_factor(mi[i].y, x1);
+      l[0] += li[i].x * e0;
+      l[1] += li[i].y * e1;
+      acc[0] += v[i].x * e0;
+      acc[1] += v[i].y * e1;
+      acc[2] += v[i].z * e0;
+      acc[3] += v[i].w * e1;
+    }
   }
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const Fragment<C> f = at(i);
-    const float2 mi = f.m(nt, c), li = f.l(nt, c);
-    const float4 v = f.acc(q, lane);
-    const float e0 = join_factor(mi.x, m[0]), e1 = join_factor(mi.y, m[1]);
-    l[0] += li.x * e0;
-    l[1] += li.y * e1;
-    acc[0] += v.x * e0;
-    acc[1] += v.y * e1;
-    acc[2] += v.z * e0;
-    acc[3] += v.w * e1;
+};
+
+// Joins n fragments for quad q, N at a time, and stores the result: as the
+// row's output (to null) or as a fragment. Fragment i lies at base + kFragment
+// (first + 2 i - (i > 0 ? back : 0)): a segment's first holder may have left
+// its second fragment, every later one left its first. Absent ones of a group
+// of N are empty.
+template <typename C, int N>
+__device__ __noinline__ void join_quad(const PagedArgs& a, const char* base, int first, int back, int n, char* to,
+                                       int32_t row, int32_t head, int q) {
+  const int lane = int(threadIdx.x & 31), nt = q / (C::D / 16), c = lane & 3;
+  Joined s;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += N) {
+    float2 mi[N], li[N];
+    float4 v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = i0 + k;
+      mi[k] = make_float2(-__builtin_huge_valf(), -__builtin_huge_valf());
+      li[k] = make_float2(0.0f, 0.0f);
+      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i < n) {
+        const Fragment<C> f{base + size_t(first + 2 * i - (i > 0 ? back : 0)) * C::kFragment};
+        mi[k] = f.m(nt, c);
+        li[k] = f.l(nt, c);
+        v[k] = f.acc(q, lane);
+      }
+    }
+    s.take<N>(mi, li, v);
   }
   if (to) {
-    store_fragment<C>(to, q, lane, acc, m, l);
+    store_fragment<C>(to, q, lane, s.acc, s.m, s.l);
   } else {
-    store_quad<C>(a, row, head, q, lane, acc, l);
-    if (q % (C::D / 16) == 0) store_lse(a, row, head, nt, lane, m, l);
+    store_quad<C>(a, row, head, q, lane, s.acc, s.l);
+    if (q % (C::D / 16) == 0) store_lse(a, row, head, nt, lane, s.m, s.l);
   }
 }
 
@@ -352,13 +416,17 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
   extern __shared__ __align__(16) char smem[];
   __shared__ Piece pieces[C::WARPS * 2];
   __shared__ int n_pieces[C::WARPS];
-  __shared__ int ids[C::WARPS];
-  __shared__ int last_of[2];
+  struct Open {  // a segment left to other CTAs as well (row -1: none)
+    int32_t row, head, cta0, cta1;
+  };
+  __shared__ Open open[2];
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31), r = lane >> 2, c = lane & 3;
   char* fragments = smem;  // two per warp
   uint4* qs = reinterpret_cast<uint4*>(smem + C::WARPS * 2 * C::kFragment + warp * C::kQuery);
   const PageView& pv = a.pages;
   const int H = pv.H;
+
+  if (threadIdx.x < 2) open[threadIdx.x].row = -1;
 
   // ---- the warp's share of the line of tiles
   const int per = (pv.n_rows + 31) / 32;
@@ -441,8 +509,14 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
       if (pv.log2P == 3) g.page[1] = i + lane < end && t + 8 < rt.len ? page_of(pv, br.slot, t + 8) : -1;
       g.full = __ballot_sync(0xffffffffu, all && (g.page[0] | g.page[1]) >= 0);
     };
-    fetch(held, cur);
-
+    float acc[C::NQ][4] = {};
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = kNone;
+      l[nt][0] = l[nt][1] = 0.0f;
+    }
+    if (rt.len > 0) {
     // query fragments, pre-split into limbs, to this warp's shared memory
     __syncwarp();
     float qf[NT][2];  // int8: what the scores of heads 2c and 2c + 1 are scaled by
@@ -451,13 +525,16 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
       const int g = nt * 8 + r;
       const int64_t qh = row * a.q.sb + (int64_t(head) * a.G + g) * a.q.sh;
       if (C::ES == 2 && QL == 1 && (a.q_vec & 2)) {  // eight bf16 as they are
+        uint4 w[D / 32];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          uint4 w = make_uint4(0, 0, 0, 0);
+          w[i] = make_uint4(0, 0, 0, 0);
           if (g < a.G)
-            w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + qh + i * 32 + c * 8));
-          qs[(nt * (D / 32) + i) * 32 + lane] = w;
+            w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + qh + i * 32 + c * 8));
         }
+        if (nt == 0) fetch(held, cur);  // the table's latency with the query's
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) qs[(nt * (D / 32) + i) * 32 + lane] = w[i];
         continue;
       }
       float x[D / 32][8];
@@ -480,6 +557,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[i][j + e] = y[e];
         }
+      if (nt == 0) fetch(held, cur);  // the table's latency with the query's
       if constexpr (C::ES == 1) {
         // a power of two brings the head's largest |q| to [2^14, 2^15)
         float top = 0.0f;
@@ -526,13 +604,6 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
     __syncwarp();  // the query's fragments and the new token's rows are visible
     fetch(held + 32, nxt);
 
-    float acc[C::NQ][4] = {};
-    float m[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = kNone;
-      l[nt][0] = l[nt][1] = 0.0f;
-    }
     int ve = 0;  // int8: see below
     float v_most = -1.0f, v_mul = 0.0f, svc[U][2];
 
@@ -863,18 +934,28 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[q][k] *= f;
     }
+    }  // rt.len > 0
     const bool whole = tile == 0 && end == rt.n;
-    char* frag = fragments + (warp * 2 + made) * C::kFragment;
+    if (whole && a.out_vec) {
+      if (a.out_dtype == FC_DTYPE_F32) store_all<C, float>(a, row, head, lane, acc, l);
+      else store_all<C, __nv_bfloat16>(a, row, head, lane, acc, l);
 #pragma unroll
-    for (int q = 0; q < C::NQ; ++q) store_fragment<C>(frag, q, lane, acc[q], m[q / MT], l[q / MT]);
-    if (whole) {
-      __syncwarp();
-      const int mine_at = warp * 2 + made;
-#pragma unroll 1
-      for (int q = 0; q < C::NQ; ++q) join_quad<C>(a, fragments, nullptr, mine_at, 1, nullptr, row, head, q);
+      for (int nt = 0; nt < NT; ++nt) store_lse(a, row, head, nt, lane, m[nt], l[nt]);
     } else {
-      if (lane == 0) pieces[warp * 2 + made] = Piece{row, head, tile, end, rt.n};
-      ++made;
+      const int mine_at = warp * 2 + made;
+#pragma unroll
+      for (int q = 0; q < C::NQ; ++q)
+        store_fragment<C>(fragments + mine_at * C::kFragment, q, lane, acc[q], m[q / MT], l[q / MT]);
+      if (whole) {  // outputs at odd addresses
+        __syncwarp();
+#pragma unroll 1
+        for (int q = 0; q < C::NQ; ++q)
+          join_quad<C, C::WARPS>(a, fragments, mine_at, 0, 1, nullptr, row, head, q);
+        __syncwarp();
+      } else {
+        if (lane == 0) pieces[mine_at] = Piece{row, head, tile, end, rt.n};
+        ++made;
+      }
     }
     at += end - tile;
     tile = 0;
@@ -883,71 +964,68 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
   if (lane == 0) n_pieces[warp] = made;
   __syncthreads();
 
-  // ---- join the CTA's fragments, segment by segment, in order
-  int open = 0;                    // segments left to other CTAs as well
-  int32_t seg_row[2], seg_head[2];
-  int32_t cta0[2], cta1[2];        // the segment's first and last CTA
+  // ---- join the CTA's fragments, segment by segment. A segment's fragments
+  // are the last one of the warp it begins in (or, where it began before this
+  // CTA, the first one of warp 0) and the first ones of the warps after it, up
+  // to the warp that ends it.
+  const int held_by = lane < C::WARPS ? n_pieces[lane] : 0;
+  const Piece p0 = pieces[2 * (lane < C::WARPS ? lane : 0)];
+  const Piece pl = pieces[held_by > 0 ? 2 * lane + held_by - 1 : 0];
+  const unsigned used = __ballot_sync(0xffffffffu, held_by > 0);
+  const unsigned ends = __ballot_sync(0xffffffffu, held_by > 0 && p0.to == p0.n);
+  // bit 0: a segment that began before; bit w + 1: one that begins in warp w
+  const unsigned starts = __ballot_sync(0xffffffffu, held_by > 0 && pl.from == 0) << 1 |
+                          (__ballot_sync(0xffffffffu, lane == 0 && held_by > 0 && p0.from > 0) ? 1u : 0u);
+  const int groups = __popc(starts), last_warp = 31 - __clz(int(used | 1u));
+  const uint32_t span = cta_chunk >> 31 ? 0x7fffffffu : uint32_t(cta_chunk);
 #pragma unroll 1
-  for (int w = 0, k = 0; w < C::WARPS;) {
-    if (k >= n_pieces[w]) {
-      ++w;
-      k = 0;
-      continue;
+  for (int i = warp; i < groups * C::NQ; i += C::WARPS) {
+    unsigned rest = starts;  // its (i / NQ)-th bit
+    for (int k = i / C::NQ; k > 0; --k) rest &= rest - 1;
+    const int bit = __ffs(int(rest)) - 1;
+    const int w0 = bit > 0 ? bit - 1 : 0, slot = bit > 0 ? 2 * w0 + n_pieces[w0] - 1 : 0;
+    const Piece first = pieces[slot];
+    int w1 = w0;
+    if (first.to < first.n) {
+      const unsigned after = ends & (0xfffffffeu << w0);
+      w1 = after ? __ffs(int(after)) - 1 : last_warp;
     }
-    const Piece first = pieces[w * 2 + k];
-    int n = 0;
-    int32_t upto = first.from;
-    // consecutive fragments of one segment: at most one per warp
-#pragma unroll 1
-    while (w < C::WARPS) {
-      if (k >= n_pieces[w]) {
-        ++w;
-        k = 0;
-        continue;
-      }
-      const Piece p = pieces[w * 2 + k];
-      if (p.row != first.row || p.head != first.head) break;
-      if (threadIdx.x == 0) ids[n] = w * 2 + k;
-      ++n;
-      upto = p.to;
-      ++k;
-    }
-    __syncthreads();
+    const int32_t upto = w1 > w0 ? pieces[2 * w1].to : first.to;
     const bool whole = first.from == 0 && upto == first.n;
     char* to_ws = a.partials + (int64_t(blockIdx.x) * 2 + (first.from > 0 ? 0 : 1)) * C::kFragment;
-#pragma unroll 1
-    for (int q = warp; q < C::NQ; q += C::WARPS)
-      join_quad<C>(a, fragments, ids, 0, n, whole ? nullptr : to_ws, first.row, first.head, q);
-    if (!whole) {
-      const int j = open++ & 1;
-      seg_row[j] = first.row;
-      seg_head[j] = first.head;
-      // its tiles before and after this CTA's, in whole CTAs
-      const uint32_t span = cta_chunk >> 31 ? 0x7fffffffu : uint32_t(cta_chunk);
-      cta0[j] = int32_t(blockIdx.x - (uint32_t(first.from) + span - 1) / span);
-      cta1[j] = int32_t(blockIdx.x + (uint32_t(first.n - upto) + span - 1) / span);
+    join_quad<C, C::WARPS>(a, fragments, slot, slot & 1, w1 - w0 + 1, whole ? nullptr : to_ws, first.row, first.head,
+                           i % C::NQ);
+    if (!whole && i % C::NQ == 0 && lane == 0) {
+      // the CTAs it lies in: its tiles before and after this one's, in shares
+      Open& o = open[first.from > 0 ? 0 : 1];
+      o.row = first.row;
+      o.head = first.head;
+      o.cta0 = int32_t(blockIdx.x - (uint32_t(first.from) + span - 1) / span);
+      o.cta1 = int32_t(blockIdx.x + (uint32_t(first.n - upto) + span - 1) / span);
     }
-    __syncthreads();
   }
-  if (open == 0) return;
+  __syncthreads();
 
-  // ---- the last CTA of a segment joins the CTAs' fragments
-  __threadfence();
+  // ---- the last CTA of a segment joins the CTAs' fragments (an atomic ticket
+  // at the segment's first CTA; the fence makes the CTA's fragments, ordered
+  // before it by the barrier, visible to the CTA that comes last)
+  if (threadIdx.x < 2 && open[threadIdx.x].row >= 0) {
+    Open& o = open[threadIdx.x];
+    __threadfence();
+    const uint32_t n = atomicAdd(&a.tickets[o.cta0], 1u);
+    if (n == uint32_t(o.cta1 - o.cta0)) {
+      a.tickets[o.cta0] = 0;
+      __threadfence();
+    } else {
+      o.row = -1;
+    }
+  }
   __syncthreads();
 #pragma unroll 1
-  for (int j = 0; j < open; ++j) {
-    const int32_t c0 = cta0[j], c1 = cta1[j];
-    if (threadIdx.x == 0) {
-      const uint32_t n = atomicAdd(&a.tickets[c0], 1u);
-      last_of[j] = n == uint32_t(c1 - c0);
-      if (last_of[j]) a.tickets[c0] = 0;
-    }
-    __syncthreads();
-    if (!last_of[j]) continue;
-    __threadfence();
-#pragma unroll 1
-    for (int q = warp; q < C::NQ; q += C::WARPS)
-      join_quad<C>(a, a.partials, nullptr, 2 * c0 + 1, c1 - c0 + 1, nullptr, seg_row[j], seg_head[j], q);
+  for (int i = warp; i < 2 * C::NQ; i += C::WARPS) {
+    const Open& o = open[i / C::NQ];
+    if (o.row >= 0)
+      join_quad<C, 8>(a, a.partials, 2 * o.cta0 + 1, 1, o.cta1 - o.cta0 + 1, nullptr, o.row, o.head, i % C::NQ);
   }
 }
 
