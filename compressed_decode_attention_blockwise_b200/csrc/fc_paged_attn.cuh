@@ -96,17 +96,20 @@ struct PagedCfg {
   static constexpr int VW = D / 8 * ES / 4;   // words of a V row per lane
   static constexpr int KL = 16 / ES < D / 4 ? 16 / ES : D / 4;  // elements per load
   static constexpr int VL = 16 / ES < D / 8 ? 16 / ES : D / 8;
-  // tiles per iteration: as many as keep 4 KB of K in flight per warp
-  static constexpr int U = KW >= 16 ? 1 : KW == 8 ? 2 : 4;
+  // tiles per iteration: more than one only where a tile is a few loads (two for
+  // int8 rows of 128 spilled: 250 us against 195 for 64 sequences of 8K)
+  static constexpr int U = KW >= 8 ? 1 : 2;
   // rows too wide for the registers are taken in parts, without prefetch
   static constexpr int kRegs = NT * D / 4 + U * (2 * KW + 4 * VW);
   static constexpr int CH = kRegs <= 192 ? 1 : kRegs <= 256 ? 2 : 4;
   static constexpr bool kPrefetch = CH == 1;
   static constexpr int NQ = NT * D / 16;      // float4 accumulators per lane
-  static constexpr int WARPS = NQ >= 32 ? 4 : kRegs <= 96 ? 12 : 8;
+  static constexpr int WARPS = NQ >= 32 ? 4 : NQ >= 16 || kRegs > 96 ? 8 : 12;
   static constexpr size_t kFragment = size_t(NQ) * 512 + NT * 64;
   static constexpr size_t kQuery = size_t(QL) * NT * (D / 32) * 512;
   static constexpr size_t kShared = WARPS * (2 * kFragment + kQuery);
+  static_assert(kShared + 600 <= 232448, "shared memory of a CTA, with the static arrays");
+  static constexpr int kMostCtas = int(WARPS * 2 * kFragment / (3 * NT * 8 * 4));  // of one segment: see the joins
 };
 
 // d += A B, or d = A B where FIRST (16 x 8 x 16; bf16, or fp16 for int8 pages).
@@ -205,187 +208,79 @@ struct RowTiles {
 // part is empty, or all its scores are NaN and have to stay so).
 __device__ __forceinline__ float join_factor(float m, float M) { return m == M ? 1.0f : fast_exp2(m - M); }
 
-// Two neighbouring outputs.
-__device__ __forceinline__ void store_pair(const PagedArgs& a, int64_t at, float x0, float x1) {
-  if (a.out_dtype == FC_DTYPE_F32) {
-    float* o = static_cast<float*>(a.out) + at;
-    if (a.out_vec) {
-      *reinterpret_cast<float2*>(o) = make_float2(x0, x1);
-    } else {
+// Writes accumulator quad q of one lane, times f0 and f1: heads 8 nt + 2c and
+// + 1, two neighbouring channels of D; any output type and alignment.
+template <typename C>
+__device__ __noinline__ void store_quad(const PagedArgs& a, int32_t row, int32_t head, int q, float4 acc, float f0,
+                                        float f1) {
+  const int lane = int(threadIdx.x & 31), r = lane >> 2, c = lane & 3;
+  const int nt = q / (C::D / 16), idx = 2 * (q % (C::D / 16));
+  const int d = idx / C::VL * 8 * C::VL + r * C::VL + idx % C::VL;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int g = nt * 8 + 2 * c + j;
+    if (g >= a.G) continue;
+    const int64_t at = row * a.os_b + (int64_t(head) * a.G + g) * a.os_h + d;
+    const float x0 = (j ? acc.y : acc.x) * (j ? f1 : f0), x1 = (j ? acc.w : acc.z) * (j ? f1 : f0);
+    if (a.out_dtype == FC_DTYPE_F32) {
+      float* o = static_cast<float*>(a.out) + at;
       o[0] = x0;
       o[1] = x1;
-    }
-  } else {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
-    if (a.out_vec) {
-      *reinterpret_cast<uint32_t*>(o) = pack_bf16(x0, x1);
+    } else if (a.out_vec) {
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at) = pack_bf16(x0, x1);
     } else {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
       o[0] = __float2bfloat16_rn(x0);
       o[1] = __float2bfloat16_rn(x1);
     }
   }
 }
 
-// Writes the accumulator quad q of one lane: heads 8 nt + 2c and + 1, two
-// neighbouring channels of D.
-template <typename C>
-__device__ __forceinline__ void store_quad(const PagedArgs& a, int32_t row, int32_t head, int q, int lane,
-                                           const float (&acc)[4], const float (&l)[2]) {
-  const int nt = q / (C::D / 16), mt = q % (C::D / 16), r = lane >> 2, c = lane & 3;
-  const int idx = 2 * mt, d = idx / C::VL * 8 * C::VL + r * C::VL + idx % C::VL;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int g = nt * 8 + 2 * c + j;
-    if (g >= a.G) continue;
-    const float inv = l[j] == 0.0f ? 0.0f : 1.0f / l[j];
-    const bool none = l[j] == 0.0f;  // an empty row's zeros
-    store_pair(a, row * a.os_b + (int64_t(head) * a.G + g) * a.os_h + d, none ? 0.0f : acc[j] * inv,
-               none ? 0.0f : acc[2 + j] * inv);
-  }
-}
-
-// The same for all quads of a segment that one warp holds whole.
+// The same for all quads of a segment that one warp holds whole, to aligned
+// outputs.
 template <typename C, typename TO>
-__device__ __forceinline__ void store_all(const PagedArgs& a, int32_t row, int32_t head, int lane,
-                                          const float (&acc)[C::NQ][4], const float (&l)[C::NT][2]) {
+__device__ __forceinline__ void store_all(const PagedArgs& a, int32_t row, int32_t head,
+                                          const float (&acc)[C::NQ][4], const float (&f)[C::NT][2]) {
   constexpr int MT = C::D / 16;
-  const int r = lane >> 2, c = lane & 3;
+  const int lane = int(threadIdx.x & 31), r = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int g = nt * 8 + 2 * c + j;
       if (g >= a.G) continue;
-      const float inv = l[nt][j] == 0.0f ? 0.0f : 1.0f / l[nt][j];
       TO* o = static_cast<TO*>(a.out) + row * a.os_b + (int64_t(head) * a.G + g) * a.os_h + r * C::VL;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const int idx = 2 * mt, d = idx / C::VL * 8 * C::VL + idx % C::VL;
-        // (an empty row's accumulators are zero)
-        const float x0 = acc[nt * MT + mt][j] * inv, x1 = acc[nt * MT + mt][2 + j] * inv;
+        const float x0 = acc[nt * MT + mt][j] * f[nt][j], x1 = acc[nt * MT + mt][2 + j] * f[nt][j];
         if constexpr (sizeof(TO) == 4) *reinterpret_cast<float2*>(o + d) = make_float2(x0, x1);
         else *reinterpret_cast<uint32_t*>(o + d) = pack_bf16(x0, x1);
       }
     }
 }
 
-// lse = ln 2 (m + log2 l) of the lane's two heads, by the lanes of row r = 0.
-__device__ __forceinline__ void store_lse(const PagedArgs& a, int32_t row, int32_t head, int nt, int lane,
-                                          const float (&m)[2], const float (&l)[2]) {
-  if (!a.lse || lane >= 4) return;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int g = nt * 8 + 2 * lane + j;
-    if (g < a.G)
-      a.lse[(int64_t(row) * a.pages.H + head) * a.G + g] =
-          l[j] == 0.0f ? __int_as_float(0xff800000) : 0.6931471805599453f * (m[j] + log2f(l[j]));
-  }
+// lse = ln 2 (m + log2 l) of query head g of a kv head's group.
+__device__ __forceinline__ void store_lse(const PagedArgs& a, int32_t row, int32_t head, int g, float m, float l) {
+  if (a.lse && g < a.G)
+    a.lse[(int64_t(row) * a.pages.H + head) * a.G + g] =
+        l == 0.0f ? -__builtin_huge_valf() : 0.6931471805599453f * (m + log2f(l));
 }
 
 // A segment's part in shared memory or the workspace: NQ x 32 float4
 // accumulators, then NT x 8 maxima (log2 domain), then NT x 8 sums.
 template <typename C>
 struct Fragment {
-  const char* p;
-  __device__ __forceinline__ float4 acc(int q, int lane) const {
-    return reinterpret_cast<const float4*>(p)[q * 32 + lane];
-  }
-  __device__ __forceinline__ float2 m(int nt, int c) const {
-    return reinterpret_cast<const float2*>(p + size_t(C::NQ) * 512)[nt * 4 + c];
-  }
-  __device__ __forceinline__ float2 l(int nt, int c) const {
-    return reinterpret_cast<const float2*>(p + size_t(C::NQ) * 512 + C::NT * 32)[nt * 4 + c];
-  }
+  char* p;
+  __device__ __forceinline__ float4& acc(int q, int lane) const { return reinterpret_cast<float4*>(p)[q * 32 + lane]; }
+  __device__ __forceinline__ float& m(int h) const { return reinterpret_cast<float*>(p + size_t(C::NQ) * 512)[h]; }
+  __device__ __forceinline__ float& l(int h) const { return m(h + C::NT * 8); }
 };
 
 // What a warp left of a segment (row, head): tiles [from, to) of n.
 struct Piece {
   int32_t row, head, from, to, n;
 };
-
-template <typename C>
-__device__ __forceinline__ void store_fragment(char* p, int q, int lane, const float (&acc)[4],
-                                               const float (&m)[2], const float (&l)[2]) {
-  reinterpret_cast<float4*>(p)[q * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-  const int nt = q / (C::D / 16);
-  if (q % (C::D / 16) == 0 && lane < 4) {
-    reinterpret_cast<float2*>(p + size_t(C::NQ) * 512)[nt * 4 + lane] = make_float2(m[0], m[1]);
-    reinterpret_cast<float2*>(p + size_t(C::NQ) * 512 + C::NT * 32)[nt * 4 + lane] = make_float2(l[0], l[1]);
-  }
-}
-
-// The running join of fragments: maxima, sums and one quad of accumulators.
-struct Joined {
-  float m[2], l[2], acc[4];
-  __device__ __forceinline__ Joined()
-      : m{-__builtin_huge_valf(), -__builtin_huge_valf()}, l{0.0f, 0.0f}, acc{0.0f, 0.0f, 0.0f, 0.0f} {}
-  // Takes N more fragments at once (the loads of all of them first).
-  template <int N>
-  __device__ __forceinline__ void take(const float2 (&mi)[N], const float2 (&li)[N], const float4 (&v)[N]) {
-    float x0 = m[0], x1 = m[1];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      x0 = fmaxf(x0, mi[i].x);
-      x1 = fmaxf(x1, mi[i].y);
-    }
-    const float f0 = join_factor(m[0], x0), f1 = join_factor(m[1], x1);
-    m[0] = x0;
-    m[1] = x1;
-    l[0] *= f0;
-    l[1] *= f1;
-    acc[0] *= f0;
-    acc[1] *= f1;
-    acc[2] *= f0;
-    acc[3] *= f1;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float e0 = join_factor(mi[i].x, x0), e1 = join_factor(mi[i].y, x1);
-      l[0] += li[i].x * e0;
-      l[1] += li[i].y * e1;
-      acc[0] += v[i].x * e0;
-      acc[1] += v[i].y * e1;
-      acc[2] += v[i].z * e0;
-      acc[3] += v[i].w * e1;
-    }
-  }
-};
-
-// Joins n fragments for quad q, N at a time, and stores the result: as the
-// row's output (to null) or as a fragment. Fragment i lies at base + kFragment
-// (first + 2 i - (i > 0 ? back : 0)): a segment's first holder may have left
-// its second fragment, every later one left its first. Absent ones of a group
-// of N are empty.
-template <typename C, int N>
-__device__ __noinline__ void join_quad(const PagedArgs& a, const char* base, int first, int back, int n, char* to,
-                                       int32_t row, int32_t head, int q) {
-  const int lane = int(threadIdx.x & 31), nt = q / (C::D / 16), c = lane & 3;
-  Joined s;
-#pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += N) {
-    float2 mi[N], li[N];
-    float4 v[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int i = i0 + k;
-      mi[k] = make_float2(-__builtin_huge_valf(), -__builtin_huge_valf());
-      li[k] = make_float2(0.0f, 0.0f);
-      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (i < n) {
-        const Fragment<C> f{base + size_t(first + 2 * i - (i > 0 ? back : 0)) * C::kFragment};
-        mi[k] = f.m(nt, c);
-        li[k] = f.l(nt, c);
-        v[k] = f.acc(q, lane);
-      }
-    }
-    s.take<N>(mi, li, v);
-  }
-  if (to) {
-    store_fragment<C>(to, q, lane, s.acc, s.m, s.l);
-  } else {
-    store_quad<C>(a, row, head, q, lane, s.acc, s.l);
-    if (q % (C::D / 16) == 0) store_lse(a, row, head, nt, lane, s.m, s.l);
-  }
-}
 
 // Four query elements at q[at ..], of either type and any alignment.
 static __device__ __noinline__ float4 load_query_slow(const void* q, int64_t at, int dtype) {
@@ -423,6 +318,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31), r = lane >> 2, c = lane & 3;
   char* fragments = smem;  // two per warp
   uint4* qs = reinterpret_cast<uint4*>(smem + C::WARPS * 2 * C::kFragment + warp * C::kQuery);
+  // (the queries' memory, once they are done with)
+  float(*factors)[NT * 8] = reinterpret_cast<float(*)[NT * 8]>(smem + C::WARPS * 2 * C::kFragment);
   const PageView& pv = a.pages;
   const int H = pv.H;
 
@@ -935,27 +832,38 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
         for (int k = 0; k < 4; ++k) acc[q][k] *= f;
     }
     }  // rt.len > 0
-    const bool whole = tile == 0 && end == rt.n;
-    if (whole && a.out_vec) {
-      if (a.out_dtype == FC_DTYPE_F32) store_all<C, float>(a, row, head, lane, acc, l);
-      else store_all<C, __nv_bfloat16>(a, row, head, lane, acc, l);
+    if (tile == 0 && end == rt.n) {
+      float f[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) store_lse(a, row, head, nt, lane, m[nt], l[nt]);
-    } else {
-      const int mine_at = warp * 2 + made;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int q = 0; q < C::NQ; ++q)
-        store_fragment<C>(fragments + mine_at * C::kFragment, q, lane, acc[q], m[q / MT], l[q / MT]);
-      if (whole) {  // outputs at odd addresses
-        __syncwarp();
-#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+          f[nt][j] = l[nt][j] == 0.0f ? 0.0f : 1.0f / l[nt][j];
+          if (r == 0) store_lse(a, row, head, nt * 8 + 2 * c + j, m[nt][j], l[nt][j]);
+        }
+      if (!a.out_vec) {
+#pragma unroll
         for (int q = 0; q < C::NQ; ++q)
-          join_quad<C, C::WARPS>(a, fragments, mine_at, 0, 1, nullptr, row, head, q);
-        __syncwarp();
+          store_quad<C>(a, row, head, q, make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]), f[q / MT][0], f[q / MT][1]);
+      } else if (a.out_dtype == FC_DTYPE_F32) {
+        store_all<C, float>(a, row, head, acc, f);
       } else {
-        if (lane == 0) pieces[mine_at] = Piece{row, head, tile, end, rt.n};
-        ++made;
+        store_all<C, __nv_bfloat16>(a, row, head, acc, f);
       }
+    } else {
+      const Fragment<C> f{fragments + (warp * 2 + made) * C::kFragment};
+#pragma unroll
+      for (int q = 0; q < C::NQ; ++q) f.acc(q, lane) = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (r == 0) {
+            f.m(nt * 8 + 2 * c + j) = m[nt][j];
+            f.l(nt * 8 + 2 * c + j) = l[nt][j];
+          }
+      if (lane == 0) pieces[warp * 2 + made] = Piece{row, head, tile, end, rt.n};
+      ++made;
     }
     at += end - tile;
     tile = 0;
@@ -978,30 +886,67 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
                           (__ballot_sync(0xffffffffu, lane == 0 && held_by > 0 && p0.from > 0) ? 1u : 0u);
   const int groups = __popc(starts), last_warp = 31 - __clz(int(used | 1u));
   const uint32_t span = cta_chunk >> 31 ? 0x7fffffffu : uint32_t(cta_chunk);
+  // the slot a segment's fragments begin at (bit: its bit in `starts`), and the
+  // warp that holds its last one
+  auto first_slot = [&](int bit) { return bit > 0 ? 2 * (bit - 1) + n_pieces[bit - 1] - 1 : 0; };
+  auto end_warp = [&](int slot) {
+    const unsigned after = ends & (0xfffffffeu << (slot >> 1));
+    return pieces[slot].to == pieces[slot].n ? slot >> 1 : after ? __ffs(int(after)) - 1 : last_warp;
+  };
+  auto upto = [&](int slot, int w1) { return pieces[w1 > slot >> 1 ? 2 * w1 : slot].to; };
+
+  // what each fragment is multiplied by: a thread per fragment and head
+  {
+    const int slot = int(threadIdx.x) / (NT * 8), h = int(threadIdx.x) % (NT * 8), w = slot >> 1;
+    if (slot < 2 * C::WARPS && (slot & 1) < n_pieces[w]) {
+      const int lead = pieces[slot].from == 0 ? slot : first_slot(31 - __clz(int(starts & ((2u << w) - 1))));
+      const int w1 = end_warp(lead), n = w1 - (lead >> 1) + 1;
+      auto at_ = [&](int i) { return Fragment<C>{fragments + (i == 0 ? lead : (lead & ~1) + 2 * i) * C::kFragment}; };
+      float M = kNone, L = 0.0f;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) M = fmaxf(M, at_(i).m(h));
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) L += at_(i).l(h) * join_factor(at_(i).m(h), M);
+      const Piece first = pieces[lead];
+      const int32_t to = upto(lead, w1);
+      const bool whole = first.from == 0 && to == first.n;
+      const float e = join_factor(Fragment<C>{fragments + slot * C::kFragment}.m(h), M);
+      factors[slot][h] = !whole ? e : L == 0.0f ? 0.0f : e / L;
+      if (slot == lead && whole) store_lse(a, first.row, first.head, h, M, L);
+      if (slot == lead && !whole) {
+        const int j = first.from > 0 ? 0 : 1;
+        const Fragment<C> f{a.partials + (int64_t(blockIdx.x) * 2 + j) * C::kFragment};
+        f.m(h) = M;
+        f.l(h) = L;
+        if (h == 0)  // the CTAs it lies in: its tiles before and after this one's
+          open[j] = Open{first.row, first.head, int32_t(blockIdx.x - (uint32_t(first.from) + span - 1) / span),
+                         int32_t(blockIdx.x + (uint32_t(first.n - to) + span - 1) / span)};
+      }
+    }
+  }
+  __syncthreads();
 #pragma unroll 1
   for (int i = warp; i < groups * C::NQ; i += C::WARPS) {
     unsigned rest = starts;  // its (i / NQ)-th bit
     for (int k = i / C::NQ; k > 0; --k) rest &= rest - 1;
-    const int bit = __ffs(int(rest)) - 1;
-    const int w0 = bit > 0 ? bit - 1 : 0, slot = bit > 0 ? 2 * w0 + n_pieces[w0] - 1 : 0;
-    const Piece first = pieces[slot];
-    int w1 = w0;
-    if (first.to < first.n) {
-      const unsigned after = ends & (0xfffffffeu << w0);
-      w1 = after ? __ffs(int(after)) - 1 : last_warp;
+    const int lead = first_slot(__ffs(int(rest)) - 1), w1 = end_warp(lead), n = w1 - (lead >> 1) + 1;
+    const int q = i % C::NQ, hc = q / MT * 8 + 2 * c;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const int slot = k == 0 ? lead : (lead & ~1) + 2 * k;
+      const float4 v = Fragment<C>{fragments + slot * C::kFragment}.acc(q, lane);
+      const float2 e = *reinterpret_cast<const float2*>(&factors[slot][hc]);
+      acc.x += v.x * e.x;
+      acc.y += v.y * e.y;
+      acc.z += v.z * e.x;
+      acc.w += v.w * e.y;
     }
-    const int32_t upto = w1 > w0 ? pieces[2 * w1].to : first.to;
-    const bool whole = first.from == 0 && upto == first.n;
-    char* to_ws = a.partials + (int64_t(blockIdx.x) * 2 + (first.from > 0 ? 0 : 1)) * C::kFragment;
-    join_quad<C, C::WARPS>(a, fragments, slot, slot & 1, w1 - w0 + 1, whole ? nullptr : to_ws, first.row, first.head,
-                           i % C::NQ);
-    if (!whole && i % C::NQ == 0 && lane == 0) {
-      // the CTAs it lies in: its tiles before and after this one's, in shares
-      Open& o = open[first.from > 0 ? 0 : 1];
-      o.row = first.row;
-      o.head = first.head;
-      o.cta0 = int32_t(blockIdx.x - (uint32_t(first.from) + span - 1) / span);
-      o.cta1 = int32_t(blockIdx.x + (uint32_t(first.n - upto) + span - 1) / span);
+    const Piece first = pieces[lead];
+    if (first.from == 0 && upto(lead, w1) == first.n) {
+      store_quad<C>(a, first.row, first.head, q, acc, 1.0f, 1.0f);
+    } else {
+      Fragment<C>{a.partials + (int64_t(blockIdx.x) * 2 + (first.from > 0 ? 0 : 1)) * C::kFragment}.acc(q, lane) = acc;
     }
   }
   __syncthreads();
@@ -1022,10 +967,61 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
   }
   __syncthreads();
 #pragma unroll 1
-  for (int i = warp; i < 2 * C::NQ; i += C::WARPS) {
-    const Open& o = open[i / C::NQ];
-    if (o.row >= 0)
-      join_quad<C, 8>(a, a.partials, 2 * o.cta0 + 1, 1, o.cta1 - o.cta0 + 1, nullptr, o.row, o.head, i % C::NQ);
+  for (int j = 0; j < 2; ++j) {
+    const Open o = open[j];
+    if (o.row < 0) continue;
+    // fragment 0 is its CTA's second, every later one its CTA's first
+    const int n = o.cta1 - o.cta0 + 1;
+    auto at_ = [&](int i) {
+      return Fragment<C>{a.partials + (int64_t(o.cta0 + i) * 2 + (i == 0 ? 1 : 0)) * C::kFragment};
+    };
+    constexpr int N = 16;  // loads in flight per lane
+    float4 v[N];
+    auto load = [&](int q, int i0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        v[k] = i0 + k < n ? at_(i0 + k).acc(q, lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    if (warp < C::NQ) load(warp, 0);  // before the factors are known
+    float* ms = reinterpret_cast<float*>(smem);  // [n][NT 8] maxima, sums, factors
+    float* ls = ms + n * NT * 8;
+    float* fs = ls + n * NT * 8;
+    for (int i = int(threadIdx.x); i < n * NT * 8; i += C::WARPS * 32) {
+      ms[i] = at_(i / (NT * 8)).m(i % (NT * 8));
+      ls[i] = at_(i / (NT * 8)).l(i % (NT * 8));
+    }
+    __syncthreads();
+    for (int i = int(threadIdx.x); i < n * NT * 8; i += C::WARPS * 32) {
+      const int h = i % (NT * 8);
+      float M = kNone, L = 0.0f;
+      for (int k = 0; k < n; ++k) M = fmaxf(M, ms[k * NT * 8 + h]);
+      for (int k = 0; k < n; ++k) L += ls[k * NT * 8 + h] * join_factor(ms[k * NT * 8 + h], M);
+      fs[i] = L == 0.0f ? 0.0f : join_factor(ms[i], M) / L;
+      if (i < NT * 8) store_lse(a, o.row, o.head, h, M, L);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int q = warp; q < C::NQ; q += C::WARPS) {
+      const int hc = q / MT * 8 + 2 * c;
+      if (q != warp) load(q, 0);
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+      for (int i0 = 0;;) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (i0 + k < n) {
+            const float2 e = *reinterpret_cast<const float2*>(&fs[(i0 + k) * NT * 8 + hc]);
+            acc.x += v[k].x * e.x;
+            acc.y += v[k].y * e.y;
+            acc.z += v[k].z * e.x;
+            acc.w += v[k].w * e.y;
+          }
+        if ((i0 += N) >= n) break;
+        load(q, i0);
+      }
+      store_quad<C>(a, o.row, o.head, q, acc, 1.0f, 1.0f);
+    }
+    __syncthreads();
   }
 }
 
@@ -1041,7 +1037,8 @@ int launch_paged(const PagedArgs& a, cudaStream_t s) {
       return FC_ERR_CUDA;
     set[dev] = true;
   }
-  kernel<<<unsigned(sm_count() * kPagedCtasPerSm), C::WARPS * 32, C::kShared, s>>>(a);
+  const int ctas = sm_count() * kPagedCtasPerSm;
+  kernel<<<unsigned(ctas < C::kMostCtas ? ctas : C::kMostCtas), C::WARPS * 32, C::kShared, s>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
