@@ -86,6 +86,8 @@ inline size_t paged_fragment_bytes(int64_t D, int64_t G) {
 
 constexpr int kTile = 16;          // tokens per tile
 constexpr float kLazy = 8.0f;      // log2 of how far p may exceed 1
+constexpr int kSetup = 1;          // what beginning a segment costs, in tiles
+constexpr int kJoin = 3;           // what a join over the workspace costs, in tiles per warp
 
 // QL, PL: limbs of the query and of P.
 template <typename T, int D_, int NT_, int QL_, int PL_>
@@ -325,13 +327,19 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
 
   if (threadIdx.x < 2) open[threadIdx.x].row = -1;
 
-  // ---- the warp's share of the line of tiles
+  // ---- the warp's share of the line of units: a segment (row, kv head) is its
+  // tiles behind kSetup units, what it costs to begin one
   const int per = (pv.n_rows + 31) / 32;
   int64_t mine = 0;
+  int32_t longest = 0;
 #pragma unroll 1
   for (int i = 0; i < per; ++i) {
     const int b = lane * per + i;
-    if (b < pv.n_rows) mine += RowTiles(pv.batch[b], a.window, a.sinks).n;
+    if (b < pv.n_rows) {
+      const int32_t n = RowTiles(pv.batch[b], a.window, a.sinks).n;
+      mine += n + kSetup;
+      longest = n > longest ? n : longest;
+    }
   }
   mine *= H;
   int64_t before = mine;  // inclusive, then exclusive prefix
@@ -342,39 +350,58 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
   }
   const int64_t total = __shfl_sync(0xffffffffu, before, 31);
   before -= mine;
-  // `chunk` tiles per warp, no fewer than U: a small batch takes fewer CTAs
-  constexpr uint32_t kFew = C::WARPS * U;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  // `chunk` units per warp, no fewer than U + kSetup: a small batch takes fewer CTAs
+  constexpr uint32_t kFew = C::WARPS * (U + kSetup);
   const uint32_t ctas = total >= int64_t(gridDim.x) * kFew ? gridDim.x : (uint32_t(total) + kFew - 1) / kFew;
   const uint32_t workers = ctas * C::WARPS;
-  const int64_t chunk = total >> 31 ? (total + workers - 1) / workers : (uint32_t(total) + workers - 1) / workers;
-  const int64_t cta_chunk = chunk * C::WARPS, cta_from = cta_chunk * blockIdx.x;
-  if (cta_from >= total) return;
-  const int64_t cta_to = cta_from + cta_chunk < total ? cta_from + cta_chunk : total;
-  const int64_t from = cta_from + chunk * warp, to = from + chunk < cta_to ? from + chunk : cta_to;
+  int64_t chunk = total >> 31 ? (total + workers - 1) / workers : (uint32_t(total) + workers - 1) / workers;
+  // A CTA per segment, if that takes its warps at most kJoin more tiles each
+  // than an even split (which joins over the workspace instead).
+  const uint32_t segments = uint32_t(pv.n_rows) * uint32_t(H);
+  const int32_t each = (longest + C::WARPS - 1) / C::WARPS;
+  const bool alone = segments <= gridDim.x && each <= chunk + kJoin;
 
-  int32_t row = 0, head = 0, tile = 0;
-  if (from < to) {
-    const unsigned who = __ballot_sync(0xffffffffu, before <= from && from < before + mine);
-    const int src = __ffs(int(who)) - 1;
-    if (lane == src) {
-      int64_t base = before;
-      row = lane * per;
+  int32_t row = 0, head = 0, unit = 0;
+  int64_t from = 0, to = 0, cta_chunk = 1;
+  if (alone) {
+    if (blockIdx.x >= segments) return;
+    row = int32_t(blockIdx.x / uint32_t(H));
+    head = int32_t(blockIdx.x % uint32_t(H));
+    const int32_t n = RowTiles(pv.batch[row], a.window, a.sinks).n, share = (n + C::WARPS - 1) / C::WARPS;
+    from = share * warp;
+    to = from + share < n ? from + share : n;
+    unit = int32_t(from) + kSetup;
+  } else {
+    cta_chunk = chunk * C::WARPS;
+    const int64_t cta_from = cta_chunk * blockIdx.x;
+    if (cta_from >= total) return;
+    const int64_t cta_to = cta_from + cta_chunk < total ? cta_from + cta_chunk : total;
+    from = cta_from + chunk * warp;
+    to = from + chunk < cta_to ? from + chunk : cta_to;
+    if (from < to) {
+      const unsigned who = __ballot_sync(0xffffffffu, before <= from && from < before + mine);
+      const int src = __ffs(int(who)) - 1;
+      if (lane == src) {
+        int64_t base = before;
+        row = lane * per;
 #pragma unroll 1
-      while (row < pv.n_rows) {
-        const int32_t n = RowTiles(pv.batch[row], a.window, a.sinks).n;
-        if (from < base + int64_t(n) * H) {
-          const int64_t x = from - base;
-          head = x >> 31 ? int32_t(x / n) : int32_t(uint32_t(x) / uint32_t(n));
-          tile = int32_t(x - int64_t(head) * n);
-          break;
+        while (row < pv.n_rows) {
+          const int32_t n = RowTiles(pv.batch[row], a.window, a.sinks).n + kSetup;
+          if (from < base + int64_t(n) * H) {
+            const int64_t x = from - base;
+            head = x >> 31 ? int32_t(x / n) : int32_t(uint32_t(x) / uint32_t(n));
+            unit = int32_t(x - int64_t(head) * n);
+            break;
+          }
+          base += int64_t(n) * H;
+          ++row;
         }
-        base += int64_t(n) * H;
-        ++row;
       }
+      row = __shfl_sync(0xffffffffu, row, src);
+      head = __shfl_sync(0xffffffffu, head, src);
+      unit = __shfl_sync(0xffffffffu, unit, src);
     }
-    row = __shfl_sync(0xffffffffu, row, src);
-    head = __shfl_sync(0xffffffffu, head, src);
-    tile = __shfl_sync(0xffffffffu, tile, src);
   }
 
   // ---- the segments of the share
@@ -384,7 +411,14 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
   while (at < to && row < pv.n_rows) {
     const BatchRow br = pv.batch[row];
     const RowTiles rt(br, a.window, a.sinks);
-    const int32_t end = int64_t(rt.n - tile) < to - at ? rt.n : tile + int32_t(to - at);
+    const int32_t last = int64_t(rt.n + kSetup - unit) < to - at ? rt.n + kSetup : unit + int32_t(to - at);
+    const int32_t tile = unit > kSetup ? unit - kSetup : 0, end = last - kSetup;
+    at += last - unit;
+    unit = 0;
+    if (end <= tile) {  // only of what comes before the tiles
+      if (last == rt.n + kSetup && ++head == H) head = 0, ++row;
+      continue;
+    }
     const int32_t Pm = (1 << pv.log2P) - 1;
 
     // The table ahead of its use: lane j holds the pages of tile held + j (-1:
@@ -540,45 +574,51 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
       }
     };
     auto load_k = [&](int32_t i, int part) {
+      auto rows = [&](auto on) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const char* p = kp + off[u][hh] + part * (KW / CH) * 16;
-          if (full || (off[u][hh] >= 0 && rt.sees(rt.start(i + u) + hh * 8 + r))) {
+          for (int hh = 0; hh < 2; ++hh) {
+            const char* p = kp + off[u][hh] + part * (KW / CH) * 16;
+            if (on(u, hh)) {
 #pragma unroll
-            for (int j = 0; j < KW / CH; j += KB / 4) load_words<KB>(&kr[u][hh][j], p + j * 16);
+              for (int j = 0; j < KW / CH; j += KB / 4) load_words<KB>(&kr[u][hh][j], p + j * 16);
+            }
+            if constexpr (C::ES == 1) {
+              const int64_t se = soff[u][hh] + head * pv.sstride_head + r;
+              if (on(u, hh)) {
+                load_words<4>(reinterpret_cast<uint32_t*>(&sk[u][hh]), pv.ks + se);
+                load_words<4>(reinterpret_cast<uint32_t*>(&sv[u][hh]), pv.vs + se);
+              } else {
+                sv[u][hh] = 0.0f;  // (a masked K row may hold anything: its score is replaced)
+              }
+            }
           }
-        }
-    };
-    auto load_scales = [&](int32_t i) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int64_t se = soff[u][hh] + head * pv.sstride_head + r;
-          if (full || (off[u][hh] >= 0 && rt.sees(rt.start(i + u) + hh * 8 + r))) {
-            load_words<4>(reinterpret_cast<uint32_t*>(&sk[u][hh]), pv.ks + se);
-            load_words<4>(reinterpret_cast<uint32_t*>(&sv[u][hh]), pv.vs + se);
-          } else {
-            sv[u][hh] = 0.0f;  // (a masked K row may hold anything: its score is replaced)
-          }
-        }
+      };
+      if (full) rows([](int, int) { return true; });
+      else rows([&](int u, int hh) { return off[u][hh] >= 0 && rt.sees(rt.start(i + u) + hh * 8 + r); });
     };
     auto load_v = [&](int32_t i, int part) {
+      auto rows = [&](auto on) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const char* p = vp + off[u][k >> 1] + (k & 1) * kRow + part * (VW / CH) * 32;
-          if (full || (off[u][k >> 1] >= 0 && rt.sees(rt.start(i + u) + (k >> 1) * 8 + 2 * c + (k & 1)))) {
+          for (int k = 0; k < 4; ++k) {
+            const char* p = vp + off[u][k >> 1] + (k & 1) * kRow + part * (VW / CH) * 32;
+            if (on(u, k)) {
 #pragma unroll
-            for (int j = 0; j < VW / CH; j += VB / 4) load_words<VB>(&vr[u][k][j], p + j * 32);
-          } else {
+              for (int j = 0; j < VW / CH; j += VB / 4) load_words<VB>(&vr[u][k][j], p + j * 32);
+            } else {
 #pragma unroll
-            for (int j = 0; j < VW / CH; ++j) vr[u][k][j] = 0;
+              for (int j = 0; j < VW / CH; ++j) vr[u][k][j] = 0;
+            }
           }
-        }
+      };
+      if (full) rows([](int, int) { return true; });
+      else
+        rows([&](int u, int k) {
+          return off[u][k >> 1] >= 0 && rt.sees(rt.start(i + u) + (k >> 1) * 8 + 2 * c + (k & 1));
+        });
     };
 
     // The first pass only loads (the loads' code is there once).
@@ -588,7 +628,6 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
       float s[U][NT][4];
       if constexpr (!C::kPrefetch) {
         advance(i);
-        if constexpr (C::ES == 1) load_scales(i);
       }
       if (work) {
         // ---- S^T = K Q^T
@@ -598,6 +637,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
           if constexpr (!C::kPrefetch) load_k(i, part);
           constexpr int STEPS = D / 16 / CH;  // k-steps of 16 channels per part
           static_assert(STEPS % 2 == 0, "two chains");
+          uint4 qb[QL][NT];  // the query's words of two k-steps
 #pragma unroll
           for (int ks = 0; ks < STEPS; ++ks) {
             const int kk = part * STEPS + ks;
@@ -630,8 +670,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
             for (int ql = 0; ql < QL; ++ql)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                const uint2 b = reinterpret_cast<const uint2*>(
-                    &qs[((ql * NT + nt) * (D / 32) + kk / 2) * 32 + lane])[kk & 1];
+                if ((kk & 1) == 0) qb[ql][nt] = qs[((ql * NT + nt) * (D / 32) + kk / 2) * 32 + lane];
+                const uint2 b = kk & 1 ? make_uint2(qb[ql][nt].z, qb[ql][nt].w) : make_uint2(qb[ql][nt].x, qb[ql][nt].y);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -697,7 +737,6 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
       if constexpr (C::kPrefetch) {
         advance(i + U);
         load_k(i + U, 0);
-        if constexpr (C::ES == 1) load_scales(i + U);
       }
       if (work) {
         // ---- running maximum, raised only where a score passes it by 2^kLazy
@@ -865,8 +904,6 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
       if (lane == 0) pieces[warp * 2 + made] = Piece{row, head, tile, end, rt.n};
       ++made;
     }
-    at += end - tile;
-    tile = 0;
     if (++head == H) head = 0, ++row;
   }
   if (lane == 0) n_pieces[warp] = made;
