@@ -611,15 +611,6 @@ def fc_select_batch(src: FcArchive, src_tail: Optional[FcTail], idx,
 
 # ------------------------------------------------------------- paged cache
 
-def _raw_stream(stream, device) -> int:
-    """cudaStream_t of the given stream, or torch's current one on device."""
-    if stream is not None:
-        return int(getattr(stream, "cuda_stream", stream))
-    if device.type != "cuda":
-        return 0
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
 def _i32(values):
     return None if values is None else \
         (ctypes.c_int32 * max(1, len(values)))(*values)
@@ -664,45 +655,8 @@ def fc_pages_compact(pages: FcPages, stream: int) -> int:
     return int(n.value)
 
 
-def fc_paged_append(pages: FcPages, layer: int, k: torch.Tensor,
-                    v: torch.Tensor, stream: int) -> None:
-    _check(load().fc_paged_append(
-        pages, layer, k.data_ptr(), v.data_ptr(), dtype_code(k.dtype),
-        _strides4(k), _strides4(v), k.shape[0], k.shape[2], stream),
-        "fc_paged_append")
-
-
 def fc_paged_workspace_bytes(Hq: int, H: int, D: int) -> int:
     return int(load().fc_paged_workspace_bytes(Hq, H, D))
-
-
-def fc_paged_attention(pages: FcPages, layer: int, q: torch.Tensor,
-                       out: torch.Tensor, lse: Optional[torch.Tensor],
-                       softmax_scale: float, window: int, sinks: int,
-                       workspace: torch.Tensor, stream: int) -> None:
-    st = load().fc_paged_attention(
-        pages, layer, q.data_ptr(), _DTYPE_CODE[q.dtype], _strides4(q),
-        q.shape[1], softmax_scale, window, sinks, workspace.data_ptr(),
-        workspace.numel(), out.data_ptr(), _DTYPE_CODE[out.dtype],
-        _strides4(out), None if lse is None else lse.data_ptr(), stream)
-    if st != FC_OK:
-        raise FcError(st, "fc_paged_attention")
-
-
-def fc_paged_step(pages: FcPages, layer: int, q: torch.Tensor,
-                  k_new: torch.Tensor, v_new: torch.Tensor, out: torch.Tensor,
-                  lse: Optional[torch.Tensor], softmax_scale: float,
-                  window: int, sinks: int, workspace: torch.Tensor,
-                  stream: int) -> None:
-    st = load().fc_paged_step(
-        pages, layer, q.data_ptr(), _DTYPE_CODE[q.dtype], _strides4(q),
-        q.shape[1], k_new.data_ptr(), v_new.data_ptr(),
-        _DTYPE_CODE[k_new.dtype], _strides4(k_new), _strides4(v_new),
-        softmax_scale, window, sinks, workspace.data_ptr(),
-        workspace.numel(), out.data_ptr(), _DTYPE_CODE[out.dtype],
-        _strides4(out), None if lse is None else lse.data_ptr(), stream)
-    if st != FC_OK:
-        raise FcError(st, "fc_paged_step")
 
 
 def fc_paged_read(pages: FcPages, layer: int, slot: int, k_out: torch.Tensor,

@@ -86,7 +86,7 @@ inline size_t paged_fragment_bytes(int64_t D, int64_t G) {
 
 constexpr int kTile = 16;          // tokens per tile
 constexpr float kLazy = 8.0f;      // log2 of how far p may exceed 1
-constexpr int kSetup = 1;          // what beginning a segment costs, in tiles
+constexpr int kSetup = 2;          // what beginning a segment costs, in tiles
 constexpr int kJoin = 3;           // what a join over the workspace costs, in tiles per warp
 
 // QL, PL: limbs of the query and of P.

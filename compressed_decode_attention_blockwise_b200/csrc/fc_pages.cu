@@ -20,9 +20,8 @@ namespace {
 
 enum RecOp : int32_t {
   kRow,    // batch[a] = {b, c, d, e}; lens[b] = c when b >= 0
-  kLen,    // lens[a] = b
   kRun,    // table[a][b + i] = c + i, i < d
-  kClear,  // table[a][b + i] = -1, i < d
+  kCrop,   // lens[a] = b; table[a][c + i] = -1, i < d
   kFork    // table[b][i] = table[a][i], i < c; lens[b] = d
 };
 struct Rec {
@@ -60,14 +59,12 @@ __global__ void __launch_bounds__(256) edit_map_kernel(const __grid_constant__ R
         if (r.b >= 0) m.lens[r.b] = r.c;
       }
       break;
-    case kLen:
-      if (lane == 0) m.lens[r.a] = r.b;
-      break;
     case kRun:
       for (int j = lane; j < r.d; j += 32) m.table[int64_t(r.a) * m.max_pages + r.b + j] = r.c + j;
       break;
-    case kClear:
-      for (int j = lane; j < r.d; j += 32) m.table[int64_t(r.a) * m.max_pages + r.b + j] = -1;
+    case kCrop:
+      for (int j = lane; j < r.d; j += 32) m.table[int64_t(r.a) * m.max_pages + r.c + j] = -1;
+      if (lane == 0) m.lens[r.a] = r.b;
       break;
     case kFork:
       for (int j = lane; j < r.c; j += 32)
@@ -357,13 +354,17 @@ int check_slots(const fc_pages* p, const int32_t* slots, int64_t n, std::vector<
   return FC_OK;
 }
 
-// Empties entries [from, to) of a slot's row.
-void drop_pages(HostEdit& ed, std::vector<Rec>& recs, int32_t slot, int64_t from, int64_t to) {
-  for (int64_t i = from; i < to; ++i) {
-    ed.drop(*ed.entry(slot, i));
-    ed.set(ed.entry(slot, i), -1);
+// Empties a slot's entries from page index `from` on (after its edit is queued).
+void drop_pages(fc_pages* p, int32_t slot, int64_t from) {
+  int32_t* row = p->h_table + int64_t(slot) * p->max_pages;
+  for (int64_t i = from, n = pages_for(p, p->h_lens[slot]); i < n; ++i) {
+    const int32_t g = row[i];
+    row[i] = -1;
+    if (--p->h_refs[g] == 0) {
+      ++p->n_free;
+      if (g < p->first_free) p->first_free = g;
+    }
   }
-  if (to > from) recs.push_back({kClear, slot, int32_t(from), 0, int32_t(to - from), 0});
 }
 
 void close_batch(fc_pages* p) {
@@ -580,20 +581,16 @@ extern "C" int fc_pages_fork(fc_pages* p, const int32_t* src, const int32_t* dst
         return FC_ERR_INVALID;
     }
     std::vector<Rec> recs;
-    HostEdit ed(p);
+    for (int64_t i = 0; i < n; ++i)
+      recs.push_back({kFork, src[i], dst[i], int32_t(pages_for(p, p->h_lens[src[i]])), p->h_lens[src[i]], 0});
+    if ((st = launch_edits(p, recs, static_cast<cudaStream_t>(stream))) != FC_OK) return st;
     for (int64_t i = 0; i < n; ++i) {
-      const int64_t m = pages_for(p, p->h_lens[src[i]]);
-      for (int64_t j = 0; j < m; ++j) {
-        const int32_t g = *ed.entry(src[i], j);
-        ed.set(&p->h_refs[g], p->h_refs[g] + 1);
-        ed.set(ed.entry(dst[i], j), g);
-      }
-      ed.set(&p->h_lens[dst[i]], p->h_lens[src[i]]);
-      recs.push_back({kFork, src[i], dst[i], int32_t(m), p->h_lens[src[i]], 0});
+      const int32_t* from = p->h_table + int64_t(src[i]) * p->max_pages;
+      int32_t* to = p->h_table + int64_t(dst[i]) * p->max_pages;
+      for (int64_t j = 0, m = pages_for(p, p->h_lens[src[i]]); j < m; ++j) ++p->h_refs[to[j] = from[j]];
+      p->h_lens[dst[i]] = p->h_lens[src[i]];
     }
     close_batch(p);
-    if ((st = launch_edits(p, recs, static_cast<cudaStream_t>(stream))) != FC_OK) return st;
-    ed.keep();
     return FC_OK;
   });
 }
@@ -606,16 +603,16 @@ extern "C" int fc_pages_free(fc_pages* p, const int32_t* slots, int64_t n, fc_st
     int st = check_slots(p, slots, n, &seen);
     if (st != FC_OK) return st;
     std::vector<Rec> recs;
-    HostEdit ed(p);
     for (int64_t i = 0; i < n; ++i) {
       if (p->h_lens[slots[i]] == 0) continue;
-      drop_pages(ed, recs, slots[i], 0, pages_for(p, p->h_lens[slots[i]]));
-      ed.set(&p->h_lens[slots[i]], 0);
-      recs.push_back({kLen, slots[i], 0, 0, 0, 0});
+      recs.push_back({kCrop, slots[i], 0, 0, int32_t(pages_for(p, p->h_lens[slots[i]])), 0});
+    }
+    if ((st = launch_edits(p, recs, static_cast<cudaStream_t>(stream))) != FC_OK) return st;
+    for (int64_t i = 0; i < n; ++i) {
+      drop_pages(p, slots[i], 0);
+      p->h_lens[slots[i]] = 0;
     }
     close_batch(p);
-    if ((st = launch_edits(p, recs, static_cast<cudaStream_t>(stream))) != FC_OK) return st;
-    ed.keep();
     return FC_OK;
   });
 }
@@ -628,15 +625,13 @@ extern "C" int fc_pages_crop(fc_pages* p, int32_t slot, int64_t tokens_to_remove
   const int64_t now = tokens_to_remove < -len ? 0 : len + tokens_to_remove;
   if (now == len) return FC_OK;
   return guarded([&]() -> int {
-    std::vector<Rec> recs;
-    HostEdit ed(p);
-    drop_pages(ed, recs, slot, pages_for(p, now), pages_for(p, len));
-    ed.set(&p->h_lens[slot], int32_t(now));
-    recs.push_back({kLen, slot, int32_t(now), 0, 0, 0});
-    close_batch(p);
+    const int64_t kept = pages_for(p, now);
+    const std::vector<Rec> recs{{kCrop, slot, int32_t(now), int32_t(kept), int32_t(pages_for(p, len) - kept), 0}};
     const int st = launch_edits(p, recs, static_cast<cudaStream_t>(stream));
     if (st != FC_OK) return st;
-    ed.keep();
+    drop_pages(p, slot, kept);
+    p->h_lens[slot] = int32_t(now);
+    close_batch(p);
     return FC_OK;
   });
 }

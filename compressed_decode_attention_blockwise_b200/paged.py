@@ -15,12 +15,15 @@ decisions and every byte of arithmetic are libfc's.
 
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
 
 from . import _lib
 
+_I64x4 = ctypes.c_int64 * 4
+_FLOAT = {torch.bfloat16: _lib.FC_DTYPE_BF16, torch.float32: _lib.FC_DTYPE_F32}
 _STORE = {"i8": torch.int8, "bf16": torch.bfloat16, "f32": torch.float32}
 
 
@@ -87,8 +90,12 @@ class PagedKVCache:
         p.batch = self._batch.data_ptr()
         p.h_table = self._h_table.data_ptr()
         p.h_lens, p.h_refs = self._h_lens.data_ptr(), self._h_refs.data_ptr()
+        self._lib = _lib.load()
+        self._ref = ctypes.byref(p)
+        self._index = -1 if device.type != "cuda" else device.index
+        self._rows = 0             # rows of the open batch (0: none)
         self._ws: dict = {}        # (stream, Hq) -> workspace
-        self._ws_bytes: dict = {}  # Hq -> bytes
+        self._dense: dict = {}     # Hq -> strides of a fresh output
         self.reset()
 
     def _check_storage(self, shape, store):
@@ -112,12 +119,13 @@ class PagedKVCache:
 
     # -- the calls' device and stream ----------------------------------------
     def _stream(self) -> int:
-        return _lib._raw_stream(None, self.device)
+        if self._index < 0:
+            return 0
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
     def _on_device(self):
         """A guard that makes the cache's device the current one."""
-        if self.device.type != "cuda" or \
-                torch.cuda.current_device() == self.device.index:
+        if self._index < 0 or torch._C._cuda_getDevice() == self._index:
             return _NO_GUARD
         return torch.cuda.device(self.device)
 
@@ -126,6 +134,7 @@ class PagedKVCache:
         """Empty every slot."""
         with self._on_device():
             _lib.fc_pages_reset(self.pages, self._stream())
+        self._rows = 0
 
     def begin(self, slots, counts=None, rows: int = 0):
         """Open the batch of a step: row i is ``slots[i]``, which grows by
@@ -144,6 +153,7 @@ class PagedKVCache:
         with self._on_device():
             _lib.fc_pages_begin(self.pages, slots, counts,
                                 rows or len(slots), self._stream())
+        self._rows = rows or len(slots)
 
     def fork(self, src, dst):
         """Slot ``dst[i]`` (empty) shares the pages of ``src[i]``."""
@@ -152,11 +162,13 @@ class PagedKVCache:
             raise ValueError("one source per destination")
         with self._on_device():
             _lib.fc_pages_fork(self.pages, src, dst, self._stream())
+        self._rows = 0
 
     def free(self, slots):
         """Empty the slots; pages no other slot shares become free."""
         with self._on_device():
             _lib.fc_pages_free(self.pages, _ints(slots), self._stream())
+        self._rows = 0
 
     def crop(self, slot: int, tokens_to_remove: int):
         """Remove the last ``-tokens_to_remove`` tokens of a slot (a negative
@@ -166,6 +178,7 @@ class PagedKVCache:
         with self._on_device():
             _lib.fc_pages_crop(self.pages, int(slot), int(tokens_to_remove),
                                self._stream())
+        self._rows = int(self.pages.n_rows)
 
     def compact(self) -> int:
         """Pack the live pages to the front of the pools; returns how many
@@ -189,6 +202,7 @@ class PagedKVCache:
                                      tuple(self._h_lens.shape)))
         with self._on_device():
             _lib.fc_pages_restore(self.pages, table, lens, self._stream())
+        self._rows = 0
 
     def seq_len(self, slot: int) -> int:
         return int(self._h_lens[slot])
@@ -200,68 +214,108 @@ class PagedKVCache:
     @property
     def rows(self) -> int:
         """Rows of the open batch (0: none)."""
-        return int(self.pages.n_rows)
+        return self._rows
 
     # -- a layer's data ------------------------------------------------------
-    def _check_tokens(self, k, v):
-        if k.dim() != 4 or k.shape != v.shape or k.shape[1] != self.Hk or \
-                k.shape[3] != self.D:
-            raise ValueError("tokens must be (B, %d, M, %d), got %s and %s"
-                             % (self.Hk, self.D, tuple(k.shape),
-                                tuple(v.shape)))
+    def _check_kind(self, k, v):
         if k.dtype != self.token_dtype or v.dtype != self.token_dtype:
             raise ValueError("tokens must be %s" % self.token_dtype)
-        if k.device != self.device or v.device != self.device:
+        if k.get_device() != self._index or v.get_device() != self._index:
             raise ValueError("tokens must be on %s" % self.device)
 
     def append(self, k: torch.Tensor, v: torch.Tensor, layer: int = 0):
         """Write the open batch's new tokens: (B, Hk, M, D), whose B * M
         tokens are the rows' new tokens in order ((1, Hk, N, D) for packed
         prompts, (rows, Hk, m, D) for m tokens each)."""
-        self._check_tokens(k, v)
+        shape = k.shape
+        if len(shape) != 4 or shape != v.shape or shape[1] != self.Hk or \
+                shape[3] != self.D:
+            raise ValueError("tokens must be (B, %d, M, %d), got %s and %s"
+                             % (self.Hk, self.D, tuple(shape),
+                                tuple(v.shape)))
+        self._check_kind(k, v)
         with self._on_device():
-            _lib.fc_paged_append(self.pages, layer, k, v, self._stream())
+            st = self._lib.fc_paged_append(
+                self._ref, layer, k.data_ptr(), v.data_ptr(),
+                _FLOAT[k.dtype], _I64x4(*k.stride()), _I64x4(*v.stride()),
+                shape[0], shape[2], self._stream())
+        if st:
+            raise _lib.FcError(st, "fc_paged_append")
 
-    def _workspace(self, Hq: int, stream: int) -> torch.Tensor:
-        n = self._ws_bytes.get(Hq)
-        if n is None:
-            n = _lib.fc_paged_workspace_bytes(Hq, self.Hk, self.D)
-            if n == 0:
-                raise _lib.FcError(_lib.FC_ERR_UNSUPPORTED,
-                                   "fc_paged_workspace_bytes")
-            self._ws_bytes[Hq] = n
-        if self.device.type == "cuda" and \
-                torch._C._cuda_isCurrentStreamCapturing():
+    def _workspace(self, Hq: int, stream: int):
+        """(tensor, address, bytes) of this stream's workspace."""
+        if self._index >= 0 and torch._C._cuda_isCurrentStreamCapturing():
             # a graph's own: graphs may be replayed side by side
-            return torch.zeros(n, dtype=torch.uint8, device=self.device)
+            return self._new_workspace(Hq)
         ws = self._ws.get((stream, Hq))
         if ws is None:
-            ws = self._ws[stream, Hq] = torch.zeros(
-                n, dtype=torch.uint8, device=self.device)
+            ws = self._ws[stream, Hq] = self._new_workspace(Hq)
         return ws
 
-    def _out(self, q, out, out_dtype, lse):
-        if q.dim() != 4 or q.shape[0] != self.pages.n_rows or \
-                q.shape[2] != 1 or q.shape[3] != self.D:
-            raise ValueError("q must be (%d, Hq, 1, %d) for the open batch, "
-                             "got %s" % (self.pages.n_rows, self.D,
-                                         tuple(q.shape)))
-        if q.device != self.device:
-            raise ValueError("q must be on %s" % self.device)
-        if q.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError("q must be bfloat16 or float32")
+    def _new_workspace(self, Hq: int):
+        n = _lib.fc_paged_workspace_bytes(Hq, self.Hk, self.D)
+        if n == 0:
+            raise _lib.FcError(_lib.FC_ERR_UNSUPPORTED,
+                               "fc_paged_workspace_bytes")
+        t = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        return t, t.data_ptr(), n
+
+    def _refuse_query(self, q):
+        raise ValueError(
+            "q must be a bfloat16 or float32 (%d, Hq, 1, %d) tensor on %s for "
+            "the open batch, got %s %s on %s" % (
+                self._rows, self.D, self.device, q.dtype, tuple(q.shape),
+                q.device))
+
+    def _attend(self, q, new, layer, out, softmax_scale, window, sinks,
+                out_dtype, lse):
+        shape = q.shape
+        code = _FLOAT.get(q.dtype)
+        if code is None or len(shape) != 4 or shape[0] != self._rows or \
+                shape[2] != 1 or shape[3] != self.D or \
+                q.get_device() != self._index:
+            self._refuse_query(q)
+        Hq = shape[1]
         if out is None:
-            out = torch.empty(q.shape, dtype=out_dtype, device=self.device)
-        elif out.shape != q.shape or out.device != self.device or \
-                out.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError("out must be a bfloat16 or float32 tensor of "
-                             "q's shape on %s" % self.device)
-        if lse is not None and (lse.shape != q.shape[:2] or
+            out = torch.empty(shape, dtype=out_dtype, device=self.device)
+            strides = self._dense.get(Hq)
+            if strides is None:
+                strides = self._dense[Hq] = _I64x4(Hq * self.D, self.D,
+                                                   self.D, 1)
+        else:
+            out_dtype = out.dtype
+            if out.shape != shape or out.get_device() != self._index:
+                raise ValueError("out must have q's shape %s, on %s"
+                                 % (tuple(shape), self.device))
+            strides = _I64x4(*out.stride())
+        out_code = _FLOAT.get(out_dtype)
+        if out_code is None:
+            raise ValueError("out must be bfloat16 or float32")
+        if lse is not None and (lse.shape != shape[:2] or
                                 lse.dtype != torch.float32 or
-                                lse.device != self.device or
+                                lse.get_device() != self._index or
                                 not lse.is_contiguous()):
             raise ValueError("lse must be a contiguous float32 (rows, Hq) "
                              "tensor on %s" % self.device)
+        with self._on_device():
+            s = self._stream()
+            ws = self._workspace(Hq, s)
+            tail = (0.0 if softmax_scale is None else softmax_scale, window,
+                    sinks, ws[1], ws[2], out.data_ptr(), out_code, strides,
+                    None if lse is None else lse.data_ptr(), s)
+            qs = _I64x4(*q.stride())
+            if new is None:
+                st = self._lib.fc_paged_attention(
+                    self._ref, layer, q.data_ptr(), code, qs, Hq, *tail)
+            else:
+                k, v = new
+                st = self._lib.fc_paged_step(
+                    self._ref, layer, q.data_ptr(), code, qs, Hq,
+                    k.data_ptr(), v.data_ptr(), _FLOAT[k.dtype],
+                    _I64x4(*k.stride()), _I64x4(*v.stride()), *tail)
+        if st:
+            raise _lib.FcError(st, "fc_paged_attention" if new is None else
+                               "fc_paged_step")
         return out
 
     def attention(self, q: torch.Tensor, layer: int = 0,
@@ -274,14 +328,8 @@ class PagedKVCache:
         ``window`` tokens and the first ``sinks`` ones. ``lse`` (rows, Hq)
         receives the log of the softmax's sum. A row without tokens gives
         zeros (lse -inf)."""
-        out = self._out(q, out, out_dtype, lse)
-        with self._on_device():
-            s = self._stream()
-            _lib.fc_paged_attention(
-                self.pages, layer, q, out, lse, 0.0 if softmax_scale is None
-                else softmax_scale, window, sinks,
-                self._workspace(q.shape[1], s), s)
-        return out
+        return self._attend(q, None, layer, out, softmax_scale, window, sinks,
+                            out_dtype, lse)
 
     def step(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
              layer: int = 0, out: Optional[torch.Tensor] = None,
@@ -290,17 +338,14 @@ class PagedKVCache:
              lse: Optional[torch.Tensor] = None) -> torch.Tensor:
         """``append`` of one token per row ((rows, Hk, 1, D)), then
         ``attention``, in one launch."""
-        self._check_tokens(k_new, v_new)
-        if k_new.shape[0] != self.pages.n_rows or k_new.shape[2] != 1:
-            raise ValueError("step takes one new token per row")
-        out = self._out(q, out, out_dtype, lse)
-        with self._on_device():
-            s = self._stream()
-            _lib.fc_paged_step(
-                self.pages, layer, q, k_new, v_new, out, lse,
-                0.0 if softmax_scale is None else softmax_scale, window,
-                sinks, self._workspace(q.shape[1], s), s)
-        return out
+        want = (self._rows, self.Hk, 1, self.D)
+        if k_new.shape != want or v_new.shape != want:
+            raise ValueError("step takes one new token per row, %s, got %s "
+                             "and %s" % (want, tuple(k_new.shape),
+                                         tuple(v_new.shape)))
+        self._check_kind(k_new, v_new)
+        return self._attend(q, (k_new, v_new), layer, out, softmax_scale,
+                            window, sinks, out_dtype, lse)
 
     def read(self, slot: int, layer: int = 0,
              dtype: Optional[torch.dtype] = None):
@@ -330,4 +375,6 @@ _NO_GUARD = _NoGuard()
 def _ints(x):
     if isinstance(x, torch.Tensor):
         x = x.tolist()
-    return [int(i) for i in x]
+    if type(x) is not list:
+        x = list(x)
+    return x
