@@ -657,11 +657,3 @@ def fc_pages_compact(pages: FcPages, stream: int) -> int:
 
 def fc_paged_workspace_bytes(Hq: int, H: int, D: int) -> int:
     return int(load().fc_paged_workspace_bytes(Hq, H, D))
-
-
-def fc_paged_read(pages: FcPages, layer: int, slot: int, k_out: torch.Tensor,
-                  v_out: torch.Tensor, stream: int) -> None:
-    _check(load().fc_paged_read(
-        pages, layer, slot, k_out.data_ptr(), v_out.data_ptr(),
-        dtype_code(k_out.dtype), _strides4(k_out), _strides4(v_out),
-        k_out.shape[2], stream), "fc_paged_read")

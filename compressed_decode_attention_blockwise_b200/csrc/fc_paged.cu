@@ -1,20 +1,22 @@
 // The paged cache's data calls: append, read, and the host side of attention
 // and the fused step. Declared in include/fc_paged.h.
 #include <climits>
+#include <type_traits>
 
 #include "fc_paged_attn.cuh"
 
 namespace fc {
 namespace {
 
-constexpr int kTokens = 8;  // new tokens per CTA of the append
 constexpr int kAppendThreads = 256;
+constexpr int kAhead = 8;  // 16-byte loads in flight per thread of a copy
 
 struct AppendArgs {
   PageView pages;
   TokenView k, v;
   int32_t dtype, vec;
-  int64_t M, offered;  // tokens per batch entry of the source, B * M
+  int64_t M, offered;    // tokens per batch entry of the source, B * M
+  int32_t ahead, side;   // tokens per thread and CTA: see the kernels
 };
 
 // The page row of new token n of the open batch, in rows of D elements from
@@ -35,27 +37,54 @@ __device__ __forceinline__ bool locate_token(const PageView& p, int64_t n, int32
   return *page >= 0;
 }
 
-// bf16 and fp32 pages: a pass of 16-byte moves (read + write, HBM-bound). A CTA
-// takes 8 tokens of all heads, K and V; its source loads are issued before the
-// pages are known, four per thread at a time.
+// Where up to N tokens of a CTA come from (element offsets of head 0) and go
+// to (page -1: nowhere), for all its threads. Thread i does token i.
+template <int N>
+struct Tokens {
+  int64_t k[N], v[N];
+  int32_t page[N], in[N];
+  __device__ __forceinline__ void sources(const AppendArgs& a, int64_t n0, int count) {
+    if (int(threadIdx.x) < count) {
+      const uint32_t n = uint32_t(n0) + threadIdx.x, M = uint32_t(a.M);  // (offered < 2^31)
+      const uint32_t b = n < M ? 0 : n / M, m = n - b * M;
+      k[threadIdx.x] = b * a.k.sb + m * a.k.sm;
+      v[threadIdx.x] = b * a.v.sb + m * a.v.sm;
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void places(const AppendArgs& a, int64_t n0, int count) {
+    if (int(threadIdx.x) < count) {
+      int32_t g = -1, i = 0;
+      if (n0 + threadIdx.x >= a.offered || !locate_token(a.pages, n0 + threadIdx.x, &g, &i)) g = -1;
+      page[threadIdx.x] = g;
+      in[threadIdx.x] = i;
+    }
+    __syncthreads();
+  }
+};
+
+// bf16 and fp32 pages: a pass of 16-byte moves (read + write, HBM-bound). A
+// thread keeps one word of one head's K or V row and takes it for `ahead`
+// tokens at once, their loads issued before the pages are known; narrow caches
+// have `side` tokens side by side in a CTA.
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int V = D * int(sizeof(T)) / 16;       // 16-byte words per row
-  constexpr int kRows = kAppendThreads / V;        // rows in flight per pass
-  __shared__ int32_t page[kTokens], in[kTokens];
-  const int64_t n0 = int64_t(blockIdx.x) * kTokens;
-  const int group = int(threadIdx.x) / V, w = int(threadIdx.x) % V;
-  const int H = a.pages.H, rows = kTokens * 2 * H;
-  bool placed = false;
-  for (int base = 0; base < rows; base += 4 * kRows) {
-    uint4 x[4];
+  constexpr int V = D * int(sizeof(T)) / 16;  // 16-byte words per row
+  __shared__ Tokens<kAppendThreads> at;
+  const int H = a.pages.H, words = 2 * H * V, count = a.ahead * a.side;
+  const int64_t n0 = int64_t(blockIdx.x) * count;
+  at.sources(a, n0, count);
+  const int sub = a.side > 1 ? int(threadIdx.x) / words : 0;
+  for (int item = int(threadIdx.x) - sub * words; item < words || item == int(threadIdx.x); item += kAppendThreads) {
+    const bool on = item < words && sub < a.side;
+    const int row = item / V, w = item % V, kv = row >= H, h = row - kv * H;
+    const TokenView& s = kv ? a.v : a.k;
+    uint4 x[kAhead];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int row = base + u * kRows + group, tok = row / (2 * H), kv = row / H & 1, h = row % H;
-      const int64_t n = n0 + tok;
-      if (row >= rows || n >= a.offered) continue;
-      const TokenView& s = kv ? a.v : a.k;
-      const T* p = static_cast<const T*>(s.p) + n / a.M * s.sb + n % a.M * s.sm + h * s.sh;
+    for (int u = 0; u < kAhead; ++u) {
+      const int t = u * a.side + sub;
+      if (!on || u >= a.ahead || n0 + t >= a.offered) continue;
+      const T* p = static_cast<const T*>(s.p) + (kv ? at.v : at.k)[t] + h * s.sh;
       if (a.vec) {
         x[u] = __ldcs(reinterpret_cast<const uint4*>(p) + w);
       } else {
@@ -72,51 +101,47 @@ __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const __gri
         x[u] = make_uint4(y[0], y[1], y[2], y[3]);
       }
     }
-    if (!placed) {
-      if (threadIdx.x < kTokens) {
-        int32_t g = -1, i = 0;
-        if (n0 + threadIdx.x >= a.offered || !locate_token(a.pages, n0 + threadIdx.x, &g, &i)) g = -1;
-        page[threadIdx.x] = g;
-        in[threadIdx.x] = i;
-      }
-      __syncthreads();
-      placed = true;
-    }
+    if (item < kAppendThreads) at.places(a, n0, count);  // (every thread's first pass)
+    T* const d = reinterpret_cast<T*>(kv ? a.pages.v : a.pages.k) + h * a.pages.stride_head;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int row = base + u * kRows + group, tok = row / (2 * H), kv = row / H & 1, h = row % H;
-      if (row >= rows || page[tok] < 0) continue;
-      T* d = reinterpret_cast<T*>(kv ? a.pages.v : a.pages.k) + page[tok] * a.pages.stride_page +
-             h * a.pages.stride_head + int64_t(in[tok]) * D;
-      reinterpret_cast<uint4*>(d)[w] = x[u];
+    for (int u = 0; u < kAhead; ++u) {
+      const int t = u * a.side + sub;
+      if (!on || u >= a.ahead || at.page[t] < 0) continue;
+      reinterpret_cast<uint4*>(d + at.page[t] * a.pages.stride_page + int64_t(at.in[t]) * D)[w] = x[u];
     }
   }
 }
 
-// int8 pages: a warp per row (token, head, K or V); see quantise_row.
+// int8 pages: a warp per row (token, head, K or V), four rows' loads at once;
+// see quantise_row.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) append_i8_kernel(const __grid_constant__ AppendArgs a) {
-  __shared__ int32_t page[kTokens], in[kTokens];
-  const int64_t n0 = int64_t(blockIdx.x) * kTokens;
-  if (threadIdx.x < kTokens) {
-    int32_t g = -1, i = 0;
-    if (n0 + threadIdx.x >= a.offered || !locate_token(a.pages, n0 + threadIdx.x, &g, &i)) g = -1;
-    page[threadIdx.x] = g;
-    in[threadIdx.x] = i;
-  }
-  __syncthreads();
+  constexpr int E = D / 32, W = kAppendThreads / 32, kRows = 4;
+  __shared__ Tokens<kAhead> at;
+  const int64_t n0 = int64_t(blockIdx.x) * a.ahead;
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
-  const int H = a.pages.H, rows = kTokens * 2 * H;
-  for (int row = warp; row < rows; row += kAppendThreads / 32) {
-    const int tok = row / (2 * H), kv = row / H & 1, h = row % H;
-    if (page[tok] < 0) continue;
-    const int64_t n = n0 + tok;
-    const TokenView& s = kv ? a.v : a.k;
-    int8_t* d = reinterpret_cast<int8_t*>(kv ? a.pages.v : a.pages.k) + page[tok] * a.pages.stride_page +
-                h * a.pages.stride_head + int64_t(in[tok]) * D;
-    float* sc = (kv ? a.pages.vs : a.pages.ks) + page[tok] * a.pages.sstride_page +
-                h * a.pages.sstride_head + in[tok];
-    store_token_row<int8_t, D>(s.p, n / a.M * s.sb + n % a.M * s.sm + h * s.sh, a.dtype, a.vec, d, sc, lane);
+  const int H = a.pages.H, rows = a.ahead * 2 * H;
+  at.sources(a, n0, a.ahead);
+  for (int base = 0; base < rows; base += kRows * W) {
+    float x[kRows][E];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int row = base + u * W + warp, tok = row / (2 * H), kv = row / H & 1, h = row % H;
+      if (row >= rows || n0 + tok >= a.offered) continue;
+      const TokenView& s = kv ? a.v : a.k;
+      load_token_row<E>(s.p, (kv ? at.v : at.k)[tok] + h * s.sh, a.dtype, a.vec, x[u], lane);
+    }
+    if (base == 0) at.places(a, n0, a.ahead);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int row = base + u * W + warp, tok = row / (2 * H), kv = row / H & 1, h = row % H;
+      if (row >= rows || at.page[tok] < 0) continue;
+      int8_t* d = reinterpret_cast<int8_t*>(kv ? a.pages.v : a.pages.k) + at.page[tok] * a.pages.stride_page +
+                  h * a.pages.stride_head + int64_t(at.in[tok]) * D;
+      float* sc = (kv ? a.pages.vs : a.pages.ks) + at.page[tok] * a.pages.sstride_page +
+                  h * a.pages.sstride_head + at.in[tok];
+      quantise_row<E>(x[u], d + lane * E, sc, lane);
+    }
   }
 }
 
@@ -128,66 +153,90 @@ struct ReadArgs {
   int32_t slot, len;
 };
 
-// Dense rows of one slot: eight elements per thread and load, four rows in
-// flight; bound by HBM (pages read + rows written).
+// Dense rows of one slot, 16-byte loads or stores, kAhead rows in flight per
+// thread; bound by HBM (pages read + rows written). Rows that keep their type
+// are moved as they are.
 template <typename T, typename TO, int D>
 __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__ ReadArgs a) {
-  constexpr int V = D / 8, kRows = 256 / V, E = 8;
+  constexpr bool kMove = std::is_same<T, TO>::value;
+  constexpr int E = kMove ? 16 / int(sizeof(T)) : 8;  // elements per thread and row
+  constexpr int V = D / E, kRows = 256 / V;
   const int group = int(threadIdx.x) / V, w = int(threadIdx.x) % V;
   const int h = int(blockIdx.y) >> 1, kv = int(blockIdx.y) & 1;
-  const int32_t t0 = int32_t(blockIdx.x) * (4 * kRows) + group;
-  float x[4][E];
-  bool on[4];
+  const int32_t t0 = int32_t(blockIdx.x) * (kAhead * kRows) + group;
+  const T* const pool = reinterpret_cast<const T*>(kv ? a.pages.v : a.pages.k) + h * a.pages.stride_head + w * E;
+  TO* const out = static_cast<TO*>(kv ? a.v : a.k) + h * (kv ? a.vs_h : a.ks_h) + w * E;
+  const int64_t os = kv ? a.vs_t : a.ks_t;
+  int32_t page[kAhead];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
+  for (int u = 0; u < kAhead; ++u) {
     const int32_t t = t0 + u * kRows;
-    const int32_t g = t < a.len ? page_of(a.pages, a.slot, t) : -1;
-    on[u] = g >= 0;
-    if (!on[u]) continue;
-    const int32_t in = t & ((1 << a.pages.log2P) - 1);
-    const T* p = reinterpret_cast<const T*>(kv ? a.pages.v : a.pages.k) + g * a.pages.stride_page +
-                 h * a.pages.stride_head + int64_t(in) * D + w * E;
-    load_vec<T, E>(p, x[u]);
-    if constexpr (sizeof(T) == 1) {
-      const float s = (kv ? a.pages.vs : a.pages.ks)[g * a.pages.sstride_page + h * a.pages.sstride_head + in];
+    page[u] = t < a.len ? page_of(a.pages, a.slot, t) : -1;
+  }
+  uint4 x[kAhead];
+  float f[kAhead][kMove ? 1 : E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[u][e] *= s;
+  for (int u = 0; u < kAhead; ++u) {
+    if (page[u] < 0) continue;
+    const int32_t in = (t0 + u * kRows) & ((1 << a.pages.log2P) - 1);
+    const T* p = pool + page[u] * a.pages.stride_page + int64_t(in) * D;
+    if constexpr (kMove) {
+      x[u] = __ldcs(reinterpret_cast<const uint4*>(p));
+    } else {
+      load_vec<T, E>(p, f[u]);
+      if constexpr (sizeof(T) == 1) {
+        const float s = (kv ? a.pages.vs : a.pages.ks)[page[u] * a.pages.sstride_page + h * a.pages.sstride_head + in];
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[u][e] *= s;
+      }
     }
   }
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    if (!on[u]) continue;
-    const int64_t t = t0 + u * kRows;
-    TO* o = static_cast<TO*>(kv ? a.v : a.k) + h * (kv ? a.vs_h : a.ks_h) + t * (kv ? a.vs_t : a.ks_t) + w * E;
-    if constexpr (sizeof(TO) == 4) {
-      reinterpret_cast<float4*>(o)[0] = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
-      reinterpret_cast<float4*>(o)[1] = make_float4(x[u][4], x[u][5], x[u][6], x[u][7]);
+  for (int u = 0; u < kAhead; ++u) {
+    if (page[u] < 0) continue;
+    TO* o = out + (t0 + u * kRows) * os;
+    if constexpr (kMove) {
+      __stcs(reinterpret_cast<uint4*>(o), x[u]);
+    } else if constexpr (sizeof(TO) == 4) {
+      reinterpret_cast<float4*>(o)[0] = make_float4(f[u][0], f[u][1], f[u][2], f[u][3]);
+      reinterpret_cast<float4*>(o)[1] = make_float4(f[u][4], f[u][5], f[u][6], f[u][7]);
     } else {
-      uint4 y;
-      y.x = pack_bf16(x[u][0], x[u][1]);
-      y.y = pack_bf16(x[u][2], x[u][3]);
-      y.z = pack_bf16(x[u][4], x[u][5]);
-      y.w = pack_bf16(x[u][6], x[u][7]);
-      *reinterpret_cast<uint4*>(o) = y;
+      *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16(f[u][0], f[u][1]), pack_bf16(f[u][2], f[u][3]),
+                                                pack_bf16(f[u][4], f[u][5]), pack_bf16(f[u][6], f[u][7]));
     }
   }
 }
 
+// Tokens per thread: eight, or two while the CTAs of eight would not fill the
+// GPU (a launch of few tokens is all latency).
 template <int D>
-int launch_append(const AppendArgs& a, int pages_dtype, unsigned grid, cudaStream_t s) {
+int launch_append(AppendArgs a, int pages_dtype, cudaStream_t s) {
+  a.ahead = a.offered < int64_t(sm_count()) * 32 ? 2 : kAhead;
+  a.side = 1;
+  if (pages_dtype != FC_DTYPE_I8) {
+    const int words = 2 * a.pages.H * (D * dtype_size(pages_dtype) / 16);
+    if (words < kAppendThreads) a.side = kAppendThreads / words;
+    if (a.side > kAppendThreads / kAhead) a.side = kAppendThreads / kAhead;
+  }
+  const int64_t per = int64_t(a.ahead) * a.side;
+  const unsigned grid = unsigned((a.offered + per - 1) / per);
   if (pages_dtype == FC_DTYPE_I8) append_i8_kernel<D><<<grid, kAppendThreads, 0, s>>>(a);
   else if (pages_dtype == FC_DTYPE_F32) append_copy_kernel<float, D><<<grid, kAppendThreads, 0, s>>>(a);
   else append_copy_kernel<__nv_bfloat16, D><<<grid, kAppendThreads, 0, s>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
+template <typename T, typename TO, int D>
+int launch_read_as(const ReadArgs& a, cudaStream_t s) {
+  constexpr int E = std::is_same<T, TO>::value ? 16 / int(sizeof(T)) : 8;
+  constexpr unsigned kTile = kAhead * 256 / (D / E);
+  const dim3 grid((unsigned(a.len) + kTile - 1) / kTile, unsigned(a.pages.H) * 2);
+  paged_read_kernel<T, TO, D><<<grid, 256, 0, s>>>(a);
+  return cuda_status(cudaGetLastError());
+}
 template <typename T, int D>
 int launch_read(const ReadArgs& a, int out_dtype, cudaStream_t s) {
-  const unsigned tile = 4 * 256 / (D / 8);
-  const dim3 grid((unsigned(a.len) + tile - 1) / tile, unsigned(a.pages.H) * 2);
-  if (out_dtype == FC_DTYPE_F32) paged_read_kernel<T, float, D><<<grid, 256, 0, s>>>(a);
-  else paged_read_kernel<T, __nv_bfloat16, D><<<grid, 256, 0, s>>>(a);
-  return cuda_status(cudaGetLastError());
+  return out_dtype == FC_DTYPE_F32 ? launch_read_as<T, float, D>(a, s) : launch_read_as<T, __nv_bfloat16, D>(a, s);
 }
 
 template <int D>
@@ -318,17 +367,16 @@ extern "C" int fc_paged_append(const fc_pages* p, int64_t layer, const void* k, 
   a.offered = B * M;
   // the grid covers every offered token, so that a captured launch serves any
   // later batch of as many
-  const unsigned grid = unsigned((B * M + kTokens - 1) / kTokens);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (p->D) {
     case 32:
-      return launch_append<32>(a, p->dtype, grid, s);
+      return launch_append<32>(a, p->dtype, s);
     case 64:
-      return launch_append<64>(a, p->dtype, grid, s);
+      return launch_append<64>(a, p->dtype, s);
     case 128:
-      return launch_append<128>(a, p->dtype, grid, s);
+      return launch_append<128>(a, p->dtype, s);
     default:
-      return launch_append<256>(a, p->dtype, grid, s);
+      return launch_append<256>(a, p->dtype, s);
   }
 }
 

@@ -122,14 +122,11 @@ __device__ __forceinline__ void quantise_row(const float (&x)[E], int8_t* dst, f
   if (lane == 0) *scale = bad ? __int_as_float(0x7fc00000) : float(double(top) / 127.0);
 }
 
-// Stores one token row (D elements of bf16 or fp32 at src[elem ..]) of one kv
-// head as the pages hold it; one warp, lane l the elements [l D/32, (l+1) D/32).
-// vec: the row is aligned for vector loads of a lane's share.
-template <typename T, int D>
-__device__ __forceinline__ void store_token_row(const void* src, int64_t elem, int src_dtype, bool vec,
-                                                T* dst, float* scale, int lane) {
-  constexpr int E = D / 32;
-  float x[E];
+// A lane's share of a token row: elements [lane E, lane E + E) of the bf16 or
+// fp32 row at src[elem ..]. vec: the row is aligned for vector loads of it.
+template <int E>
+__device__ __forceinline__ void load_token_row(const void* src, int64_t elem, int src_dtype, bool vec,
+                                               float (&x)[E], int lane) {
   if (vec && src_dtype == FC_DTYPE_BF16) {
     load_vec<__nv_bfloat16, E>(static_cast<const __nv_bfloat16*>(src) + elem + lane * E, x);
   } else if (vec) {
@@ -138,6 +135,15 @@ __device__ __forceinline__ void store_token_row(const void* src, int64_t elem, i
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] = load_any(src, elem + lane * E + i, src_dtype);
   }
+}
+
+// Stores one token row of one kv head as the pages hold it (one warp).
+template <typename T, int D>
+__device__ __forceinline__ void store_token_row(const void* src, int64_t elem, int src_dtype, bool vec,
+                                                T* dst, float* scale, int lane) {
+  constexpr int E = D / 32;
+  float x[E];
+  load_token_row<E>(src, elem, src_dtype, vec, x, lane);
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < E; ++i) dst[lane * E + i] = x[i];

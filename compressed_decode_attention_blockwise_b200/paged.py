@@ -75,6 +75,7 @@ class PagedKVCache:
         self._h_table = torch.full((n_slots, self.max_pages), -1, **i32)
         self._h_lens = torch.zeros(n_slots, **i32)
         self._h_refs = torch.zeros(n_pages, **i32)
+        self._np_lens = self._h_lens.numpy()
         p = self.pages = _lib.FcPages()
         p.k, p.v = self.k.data_ptr(), self.v.data_ptr()
         if self.k_scales is not None:
@@ -205,7 +206,7 @@ class PagedKVCache:
         self._rows = 0
 
     def seq_len(self, slot: int) -> int:
-        return int(self._h_lens[slot])
+        return int(self._np_lens[slot])
 
     @property
     def free_pages(self) -> int:
@@ -351,13 +352,20 @@ class PagedKVCache:
              dtype: Optional[torch.dtype] = None):
         """(k, v) of one slot as dense (1, Hk, seq_len, D) rows in the token
         dtype (or ``dtype``)."""
-        shape = (1, self.Hk, self.seq_len(slot), self.D)
         dt = dtype or self.token_dtype
-        k = torch.empty(shape, dtype=dt, device=self.device)
-        v = torch.empty(shape, dtype=dt, device=self.device)
+        code = _FLOAT.get(dt)
+        if code is None:
+            raise ValueError("rows are read as bfloat16 or float32")
+        T = self.seq_len(slot)
+        k, v = torch.empty((2, 1, self.Hk, T, self.D), dtype=dt,
+                           device=self.device).unbind(0)
+        strides = _I64x4(self.Hk * T * self.D, T * self.D, self.D, 1)
         with self._on_device():
-            _lib.fc_paged_read(self.pages, layer, int(slot), k, v,
-                               self._stream())
+            st = self._lib.fc_paged_read(
+                self._ref, layer, slot, k.data_ptr(), v.data_ptr(), code,
+                strides, strides, T, self._stream())
+        if st:
+            raise _lib.FcError(st, "fc_paged_read")
         return k, v
 
 
