@@ -137,21 +137,17 @@ __device__ __forceinline__ void load_token_row(const void* src, int64_t elem, in
   }
 }
 
-// Stores one token row of one kv head as the pages hold it (one warp).
-template <typename T, int D>
-__device__ __forceinline__ void store_token_row(const void* src, int64_t elem, int src_dtype, bool vec,
-                                                T* dst, float* scale, int lane) {
-  constexpr int E = D / 32;
-  float x[E];
-  load_token_row<E>(src, elem, src_dtype, vec, x, lane);
+// Stores a lane's share of a token row as the pages hold it (a warp per row).
+template <typename T, int E>
+__device__ __forceinline__ void store_row(const float (&x)[E], T* dst, float* scale, int lane) {
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) dst[lane * E + i] = x[i];
+    for (int i = 0; i < E; ++i) dst[i] = x[i];
   } else if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) dst[lane * E + i] = __float2bfloat16_rn(x[i]);
+    for (int i = 0; i < E; ++i) dst[i] = __float2bfloat16_rn(x[i]);
   } else {
-    quantise_row<E>(x, dst + lane * E, scale, lane);
+    quantise_row<E>(x, dst, scale, lane);
   }
 }
 

@@ -111,7 +111,7 @@ struct PagedCfg {
   static constexpr size_t kQuery = size_t(QL) * NT * (D / 32) * 512;
   static constexpr size_t kShared = WARPS * (2 * kFragment + kQuery);
   static_assert(kShared + 600 <= 232448, "shared memory of a CTA, with the static arrays");
-  static constexpr int kMostCtas = int(WARPS * 2 * kFragment / (3 * NT * 8 * 4));  // of one segment: see the joins
+  static constexpr int kMostCtas = int(WARPS * 2 * kFragment / (NT * 8 * 4));  // of one segment: see the joins
 };
 
 // d += A B, or d = A B where FIRST (16 x 8 x 16; bf16, or fp16 for int8 pages).
@@ -290,16 +290,23 @@ static __device__ __noinline__ float4 load_query_slow(const void* q, int64_t at,
                      load_any(q, at + 3, dtype));
 }
 
-// The new token's K (kv = 0) or V row of a kv head, to its page.
+// The new token's K and V rows of a kv head, to their page.
 template <typename T, int D>
-__device__ __noinline__ void store_new_row(const PagedArgs& a, int32_t row, int32_t head, int64_t page,
-                                           int32_t in, int kv) {
+__device__ __noinline__ void store_new_rows(const PagedArgs& a, int32_t row, int32_t head, int64_t page, int32_t in) {
+  constexpr int E = D / 32;
   const PageView& pv = a.pages;
-  const TokenView& s = kv ? a.vn : a.kn;
-  T* d = reinterpret_cast<T*>(kv ? pv.v : pv.k) + page * pv.stride_page + head * pv.stride_head + int64_t(in) * D;
-  float* sc = (kv ? pv.vs : pv.ks) + page * pv.sstride_page + head * pv.sstride_head + in;
-  store_token_row<T, D>(s.p, row * s.sb + head * s.sh, a.new_dtype, a.new_vec >> kv & 1, d, sc,
-                        int(threadIdx.x & 31));
+  const int lane = int(threadIdx.x & 31);
+  float x[2][E];
+  load_token_row<E>(a.kn.p, row * a.kn.sb + head * a.kn.sh, a.new_dtype, a.new_vec & 1, x[0], lane);
+  load_token_row<E>(a.vn.p, row * a.vn.sb + head * a.vn.sh, a.new_dtype, a.new_vec & 2, x[1], lane);
+  const int64_t at = page * pv.stride_page + head * pv.stride_head + int64_t(in) * D + lane * E;
+  const int64_t se = page * pv.sstride_page + head * pv.sstride_head + in;
+#pragma unroll 1
+  for (int kv = 0; kv < 2; ++kv) {
+    store_row<T, E>(x[0], reinterpret_cast<T*>(kv ? pv.v : pv.k) + at, (kv ? pv.vs : pv.ks) + se, lane);
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[0][i] = x[1][i];
+  }
 }
 
 template <typename T, int D, int NT, int QL, int PL>
@@ -527,10 +534,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
       // the fused append: the warp with the segment's last tile stores the new
       // token's rows, which no other warp reads
       const int32_t page = page_of(pv, br.slot, rt.len - 1);
-      if (page >= 0) {
-        store_new_row<T, D>(a, row, head, page, (rt.len - 1) & Pm, 0);
-        store_new_row<T, D>(a, row, head, page, (rt.len - 1) & Pm, 1);
-      }
+      if (page >= 0) store_new_rows<T, D>(a, row, head, page, (rt.len - 1) & Pm);
     }
     __syncwarp();  // the query's fragments and the new token's rows are visible
     fetch(held + 32, nxt);
@@ -1020,21 +1024,19 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
         v[k] = i0 + k < n ? at_(i0 + k).acc(q, lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     };
     if (warp < C::NQ) load(warp, 0);  // before the factors are known
-    float* ms = reinterpret_cast<float*>(smem);  // [n][NT 8] maxima, sums, factors
-    float* ls = ms + n * NT * 8;
-    float* fs = ls + n * NT * 8;
-    for (int i = int(threadIdx.x); i < n * NT * 8; i += C::WARPS * 32) {
-      ms[i] = at_(i / (NT * 8)).m(i % (NT * 8));
-      ls[i] = at_(i / (NT * 8)).l(i % (NT * 8));
-    }
-    __syncthreads();
-    for (int i = int(threadIdx.x); i < n * NT * 8; i += C::WARPS * 32) {
-      const int h = i % (NT * 8);
+    float* fs = reinterpret_cast<float*>(smem);  // [n][NT 8], by a warp per head
+#pragma unroll 1
+    for (int h = warp; h < NT * 8; h += C::WARPS) {
       float M = kNone, L = 0.0f;
-      for (int k = 0; k < n; ++k) M = fmaxf(M, ms[k * NT * 8 + h]);
-      for (int k = 0; k < n; ++k) L += ls[k * NT * 8 + h] * join_factor(ms[k * NT * 8 + h], M);
-      fs[i] = L == 0.0f ? 0.0f : join_factor(ms[i], M) / L;
-      if (i < NT * 8) store_lse(a, o.row, o.head, h, M, L);
+#pragma unroll 1
+      for (int k = lane; k < n; k += 32) M = fmaxf(M, at_(k).m(h));
+      M = warp_max(M);
+#pragma unroll 1
+      for (int k = lane; k < n; k += 32) L += at_(k).l(h) * join_factor(at_(k).m(h), M);
+      L = warp_sum(L);
+#pragma unroll 1
+      for (int k = lane; k < n; k += 32) fs[k * NT * 8 + h] = L == 0.0f ? 0.0f : join_factor(at_(k).m(h), M) / L;
+      if (lane == 0) store_lse(a, o.row, o.head, h, M, L);
     }
     __syncthreads();
 #pragma unroll 1
