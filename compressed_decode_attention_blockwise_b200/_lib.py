@@ -8,6 +8,7 @@ missing library is an error, never a fallback.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional
@@ -611,9 +612,14 @@ def fc_select_batch(src: FcArchive, src_tail: Optional[FcTail], idx,
 
 # ------------------------------------------------------------- paged cache
 
-def _i32(values):
-    return None if values is None else \
-        (ctypes.c_int32 * max(1, len(values)))(*values)
+class _Ints:
+    """A host int32 array of a list (array.array converts several times
+    faster than a ctypes array does)."""
+    __slots__ = ("a", "p")
+
+    def __init__(self, values):
+        self.a = None if values is None else array.array("i", values)
+        self.p = None if values is None else self.a.buffer_info()[0]
 
 
 def fc_pages_reset(pages: FcPages, stream: int) -> None:
@@ -628,17 +634,20 @@ def fc_pages_restore(pages: FcPages, table: torch.Tensor, lens: torch.Tensor,
 
 def fc_pages_begin(pages: FcPages, slots, counts, n_rows: int,
                    stream: int) -> None:
-    _check(load().fc_pages_begin(pages, _i32(slots), _i32(counts), len(slots),
-                                 n_rows, stream), "fc_pages_begin")
+    s, c = _Ints(slots), _Ints(counts)
+    _check(load().fc_pages_begin(pages, s.p, c.p, len(slots), n_rows, stream),
+           "fc_pages_begin")
 
 
 def fc_pages_fork(pages: FcPages, src, dst, stream: int) -> None:
-    _check(load().fc_pages_fork(pages, _i32(src), _i32(dst), len(dst),
-                                stream), "fc_pages_fork")
+    s, d = _Ints(src), _Ints(dst)
+    _check(load().fc_pages_fork(pages, s.p, d.p, len(dst), stream),
+           "fc_pages_fork")
 
 
 def fc_pages_free(pages: FcPages, slots, stream: int) -> None:
-    _check(load().fc_pages_free(pages, _i32(slots), len(slots), stream),
+    s = _Ints(slots)
+    _check(load().fc_pages_free(pages, s.p, len(slots), stream),
            "fc_pages_free")
 
 

@@ -278,7 +278,8 @@ class PagedKVCache:
             self._refuse_query(q)
         Hq = shape[1]
         if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=self.device)
+            out = torch.empty_like(q, dtype=out_dtype,
+                                   memory_format=torch.contiguous_format)
             strides = self._dense.get(Hq)
             if strides is None:
                 strides = self._dense[Hq] = _I64x4(Hq * self.D, self.D,
@@ -298,22 +299,28 @@ class PagedKVCache:
                                 not lse.is_contiguous()):
             raise ValueError("lse must be a contiguous float32 (rows, Hq) "
                              "tensor on %s" % self.device)
-        with self._on_device():
+        guard = self._on_device()
+        guard.__enter__()
+        try:
             s = self._stream()
-            ws = self._workspace(Hq, s)
-            tail = (0.0 if softmax_scale is None else softmax_scale, window,
-                    sinks, ws[1], ws[2], out.data_ptr(), out_code, strides,
-                    None if lse is None else lse.data_ptr(), s)
-            qs = _I64x4(*q.stride())
+            _, ws, ws_bytes = self._workspace(Hq, s)
+            scale = 0.0 if softmax_scale is None else softmax_scale
+            lse_ptr = None if lse is None else lse.data_ptr()
             if new is None:
                 st = self._lib.fc_paged_attention(
-                    self._ref, layer, q.data_ptr(), code, qs, Hq, *tail)
+                    self._ref, layer, q.data_ptr(), code, _I64x4(*q.stride()),
+                    Hq, scale, window, sinks, ws, ws_bytes, out.data_ptr(),
+                    out_code, strides, lse_ptr, s)
             else:
                 k, v = new
                 st = self._lib.fc_paged_step(
-                    self._ref, layer, q.data_ptr(), code, qs, Hq,
-                    k.data_ptr(), v.data_ptr(), _FLOAT[k.dtype],
-                    _I64x4(*k.stride()), _I64x4(*v.stride()), *tail)
+                    self._ref, layer, q.data_ptr(), code, _I64x4(*q.stride()),
+                    Hq, k.data_ptr(), v.data_ptr(), _FLOAT[k.dtype],
+                    _I64x4(*k.stride()), _I64x4(*v.stride()), scale, window,
+                    sinks, ws, ws_bytes, out.data_ptr(), out_code, strides,
+                    lse_ptr, s)
+        finally:
+            guard.__exit__(None, None, None)
         if st:
             raise _lib.FcError(st, "fc_paged_attention" if new is None else
                                "fc_paged_step")
