@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const __gri
   __shared__ Tokens<kAppendThreads> at;
   const int H = a.pages.H, words = 2 * H * V, count = a.ahead * a.side;
   const int64_t n0 = int64_t(blockIdx.x) * count;
+  after_previous();
   at.sources(a, n0, count);
   const int sub = a.side > 1 ? int(threadIdx.x) / words : 0;
   for (int item = int(threadIdx.x) - sub * words; item < words || item == int(threadIdx.x); item += kAppendThreads) {
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_i8_kernel(const __grid_
   const int64_t n0 = int64_t(blockIdx.x) * a.ahead;
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
   const int H = a.pages.H, rows = a.ahead * 2 * H;
+  after_previous();
   at.sources(a, n0, a.ahead);
   for (int base = 0; base < rows; base += kRows * W) {
     float x[kRows][E];
@@ -168,6 +170,7 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__
   TO* const out = static_cast<TO*>(kv ? a.v : a.k) + h * (kv ? a.vs_h : a.ks_h) + w * E;
   const int64_t os = kv ? a.vs_t : a.ks_t;
   int32_t page[kAhead];
+  after_previous();
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) {
     const int32_t t = t0 + u * kRows;
@@ -220,10 +223,10 @@ int launch_append(AppendArgs a, int pages_dtype, cudaStream_t s) {
   }
   const int64_t per = int64_t(a.ahead) * a.side;
   const unsigned grid = unsigned((a.offered + per - 1) / per);
-  if (pages_dtype == FC_DTYPE_I8) append_i8_kernel<D><<<grid, kAppendThreads, 0, s>>>(a);
-  else if (pages_dtype == FC_DTYPE_F32) append_copy_kernel<float, D><<<grid, kAppendThreads, 0, s>>>(a);
-  else append_copy_kernel<__nv_bfloat16, D><<<grid, kAppendThreads, 0, s>>>(a);
-  return cuda_status(cudaGetLastError());
+  auto* kernel = pages_dtype == FC_DTYPE_I8    ? append_i8_kernel<D>
+                 : pages_dtype == FC_DTYPE_F32 ? append_copy_kernel<float, D>
+                                               : append_copy_kernel<__nv_bfloat16, D>;
+  return launch_after(kernel, dim3(grid), kAppendThreads, 0, s, a);
 }
 
 template <typename T, typename TO, int D>
@@ -231,8 +234,7 @@ int launch_read_as(const ReadArgs& a, cudaStream_t s) {
   constexpr int E = std::is_same<T, TO>::value ? 16 / int(sizeof(T)) : 8;
   constexpr unsigned kTile = kAhead * 256 / (D / E);
   const dim3 grid((unsigned(a.len) + kTile - 1) / kTile, unsigned(a.pages.H) * 2);
-  paged_read_kernel<T, TO, D><<<grid, 256, 0, s>>>(a);
-  return cuda_status(cudaGetLastError());
+  return launch_after(paged_read_kernel<T, TO, D>, grid, 256, 0, s, a);
 }
 template <typename T, int D>
 int launch_read(const ReadArgs& a, int out_dtype, cudaStream_t s) {

@@ -43,7 +43,35 @@ struct TokenView {
   int64_t sb, sh, sm;
 };
 
+// Launches a kernel that may be set up while the kernel before it on the stream
+// still runs (a programmatic dependent): its blocks begin with after_previous(),
+// which waits until that kernel is complete and its writes are visible, so only
+// the launch itself overlaps. A launch of this file saves about a microsecond
+// behind another one.
+template <typename Arg>
+inline int launch_after(void (*kernel)(Arg), dim3 grid, unsigned block, size_t smem, cudaStream_t stream,
+                        const Arg& arg) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, arg));
+}
+
 // ------------------------------------------------------------------ device
+
+// The first thing every block of a launch_after kernel does: nothing of global
+// memory may be touched before it. It then lets the next launch be set up.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // The page that holds position t of a slot, -1 when the map has none (so that
 // a stale map masks the token instead of sending a load astray).

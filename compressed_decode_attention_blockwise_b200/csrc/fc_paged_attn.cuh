@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
   const PageView& pv = a.pages;
   const int H = pv.H;
 
+  after_previous();
   if (threadIdx.x < 2) open[threadIdx.x].row = -1;
 
   // ---- the warp's share of the line of units: a segment (row, kv head) is its
@@ -1077,8 +1078,8 @@ int launch_paged(const PagedArgs& a, cudaStream_t s) {
     set[dev] = true;
   }
   const int ctas = sm_count() * kPagedCtasPerSm;
-  kernel<<<unsigned(ctas < C::kMostCtas ? ctas : C::kMostCtas), C::WARPS * 32, C::kShared, s>>>(a);
-  return cuda_status(cudaGetLastError());
+  return launch_after(kernel, dim3(unsigned(ctas < C::kMostCtas ? ctas : C::kMostCtas)), C::WARPS * 32, C::kShared, s,
+                      a);
 }
 
 template <typename T, int QL, int PL>

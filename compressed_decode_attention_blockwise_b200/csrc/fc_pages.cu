@@ -49,6 +49,7 @@ struct Recs {
 template <int N>
 __global__ void __launch_bounds__(256) edit_map_kernel(const __grid_constant__ Recs<N> p) {
   const int i = int(blockIdx.x) * 8 + int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+  after_previous();
   if (i >= p.n) return;
   const Rec r = p.r[i];
   const MapView& m = p.m;
@@ -80,8 +81,7 @@ int launch_recs(const MapView& m, const Rec* r, int n, cudaStream_t s) {
   a.m = m;
   a.n = n;
   for (int i = 0; i < n; ++i) a.r[i] = r[i];
-  edit_map_kernel<N><<<unsigned((n + 7) / 8), 256, 0, s>>>(a);
-  return cuda_status(cudaGetLastError());
+  return launch_after(edit_map_kernel<N>, dim3(unsigned((n + 7) / 8)), 256, 0, s, a);
 }
 
 int launch_edits(const fc_pages* p, const std::vector<Rec>& recs, cudaStream_t s) {
@@ -131,6 +131,7 @@ constexpr int kPieceBytes = 4096;
 template <int N>
 __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__ Pairs<N> a) {
   const CopyShape& s = a.s;
+  after_previous();
   const int lane = int(threadIdx.x & 31);
   if (blockIdx.x >= s.copy_blocks) {
     __shared__ Pair sp[N];
@@ -195,8 +196,7 @@ int launch_pairs(const CopyShape& shape, const Pair* pr, int n, cudaStream_t str
     blocks += t > 64 ? 64 : t;
     a.s.first_moved = pr[0].src;
   }
-  copy_pages_kernel<N><<<unsigned(blocks), 256, 0, stream>>>(a);
-  return cuda_status(cudaGetLastError());
+  return launch_after(copy_pages_kernel<N>, dim3(unsigned(blocks)), 256, 0, stream, a);
 }
 
 int launch_copies(const fc_pages* p, const std::vector<Pair>& pairs, bool remap, cudaStream_t stream) {
@@ -251,6 +251,7 @@ struct MapChunk {
 
 __global__ void __launch_bounds__(128) upload_map_kernel(const __grid_constant__ MapChunk c) {
   const auto& g = c.seg[blockIdx.x];
+  after_previous();
   int32_t* to = g.slot < 0 ? c.m.lens + g.at : c.m.table + int64_t(g.slot) * c.m.max_pages + g.at;
   for (int i = int(threadIdx.x); i < g.n; i += 128) to[i] = c.v[g.off + i];
 }
@@ -265,9 +266,9 @@ struct MapUpload {
   }
   int flush() {
     if (c.n == 0) return FC_OK;
-    upload_map_kernel<<<unsigned(c.n), 128, 0, s>>>(c);
+    const int st = launch_after(upload_map_kernel, dim3(unsigned(c.n)), 128, 0, s, c);
     c.n = used = 0;
-    return cuda_status(cudaGetLastError());
+    return st;
   }
   int add(int32_t slot, const int32_t* v, int64_t n) {
     for (int64_t at = 0; at < n;) {
