@@ -106,7 +106,7 @@ struct PagedCfg {
   static constexpr int CH = kRegs <= 192 ? 1 : kRegs <= 256 ? 2 : 4;
   static constexpr bool kPrefetch = CH == 1;
   static constexpr int NQ = NT * D / 16;      // float4 accumulators per lane
-  static constexpr int WARPS = NQ >= 32 ? 4 : NQ >= 16 || kRegs > 96 ? 8 : 12;
+  static constexpr int WARPS = NQ >= 32 ? 4 : NQ >= 16 || kRegs > 96 ? 8 : kRegs > 64 || NT > 1 ? 12 : 16;
   static constexpr size_t kFragment = size_t(NQ) * 512 + NT * 64;
   static constexpr size_t kQuery = size_t(QL) * NT * (D / 32) * 512;
   static constexpr size_t kShared = WARPS * (2 * kFragment + kQuery);
