@@ -140,7 +140,7 @@ class FcPages(ctypes.Structure):
         ("h_refs", ctypes.c_void_p),
         ("first_free", ctypes.c_int64), ("n_free", ctypes.c_int64),
         ("n_rows", ctypes.c_int64), ("n_tokens", ctypes.c_int64),
-        ("one_each", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("one_each", ctypes.c_int32), ("device_rows", ctypes.c_int32),
     ]
 
 

@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
           // exponent of every scale so far, so that fp16 holds them (p <= 2^8)
           float x = 0.0f;
 #pragma unroll
-          for (int u = 0; u < U; ++u) x = fmaxf(x, fmaxf(sv[u][0], sv[u][1]));
+          for (int u = 0; u < U; ++u) x = fmaxf(x, fmaxf(fabsf(sv[u][0]), fabsf(sv[u][1])));
           if (__any_sync(0xffffffffu, x > v_most)) {
             x = warp_max(x);
             int e = exponent_of(x) + 1;

@@ -453,12 +453,14 @@ extern "C" int fc_pages_reset(fc_pages* p, fc_stream stream) {
   const size_t entries = size_t(p->n_slots) * size_t(p->max_pages);
   cudaError_t e = cudaMemsetAsync(p->table, 0xff, entries * 4, s);
   if (e == cudaSuccess) e = cudaMemsetAsync(p->lens, 0, size_t(p->n_slots) * 4, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(p->batch, 0xff, size_t(p->n_slots) * 16, s);  // slot -1
   if (e != cudaSuccess) return FC_ERR_CUDA;
   for (size_t i = 0; i < entries; ++i) p->h_table[i] = -1;
   for (int64_t i = 0; i < p->n_slots; ++i) p->h_lens[i] = 0;
   for (int64_t i = 0; i < p->n_pages; ++i) p->h_refs[i] = 0;
   p->first_free = 0;
   p->n_free = p->n_pages;
+  p->device_rows = 0;
   close_batch(p);
   return FC_OK;
 }
@@ -557,8 +559,11 @@ extern "C" int fc_pages_begin(fc_pages* p, const int32_t* slots, const int32_t* 
       recs.push_back({kRow, int32_t(i), slot, now, first, c});
       first += c;
     }
-    for (int64_t i = n; i < n_rows; ++i) recs.push_back({kRow, int32_t(i), -1, 0, first, 0});
+    // padding, and what a larger batch left behind (a captured launch may read it)
+    const int64_t rows = p->device_rows > n_rows ? p->device_rows : n_rows;
+    for (int64_t i = n; i < rows; ++i) recs.push_back({kRow, int32_t(i), -1, 0, first, 0});
     p->n_rows = n_rows;
+    p->device_rows = int32_t(n_rows);
     p->n_tokens = total;
     p->one_each = one_each ? 1 : 0;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);

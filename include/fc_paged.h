@@ -32,7 +32,9 @@
  *     being captured is FC_ERR_INVALID.
  *   - The batch of the current step (fc_pages_begin) is device data too, so a
  *     captured graph of fc_paged_append / _attention / _step launches may be
- *     replayed after each fc_pages_begin with as many rows.
+ *     replayed after each fc_pages_begin with at most as many rows (the rows
+ *     past them are then empty). A replay without a new batch repeats the last
+ *     one: it must not follow a fork, free or crop of its slots.
  *   - Queue all calls of one cache on one stream, or order the streams.
  *
  * Supported sizes: D in {32, 64, 128, 256}; Hq a multiple of H with G = Hq / H
@@ -66,8 +68,9 @@ extern "C" {
  *   first_free, n_free   no page below first_free is free; free pages.
  *   n_rows, n_tokens, one_each   the open batch (host): its rows, its new
  *               tokens, whether every row has exactly one; n_rows == 0: none.
- * fc_pages_reset or fc_pages_restore sets the map and the host fields; they
- * are the library's from then on.
+ *   device_rows   rows of `batch` that may not be empty on the device.
+ * fc_pages_reset, the first call on a new cache, sets the map and the host
+ * fields; they are the library's from then on.
  */
 typedef struct fc_pages {
   void* k;
@@ -89,7 +92,7 @@ typedef struct fc_pages {
   int64_t first_free, n_free;
   int64_t n_rows, n_tokens;
   int32_t one_each;
-  int32_t reserved;
+  int32_t device_rows;
 } fc_pages;
 
 /* fc_pages_reset -- empty every slot: all pages free, tables -1, no batch. */
@@ -160,7 +163,7 @@ int fc_pages_compact(fc_pages* p, int64_t* n_live, fc_stream stream);
  *   k, v      device, (B, H, M, D) of dtype with element strides [4],
  *             innermost 1: new token j of the batch (rows in order, each
  *             row's tokens in order) is element (j / M, :, j mod M, :).
- *             B * M >= the batch's new tokens; further elements are not read.
+ *             B * M >= the batch's new tokens; further elements are ignored.
  *   dtype     the pages' dtype; FC_DTYPE_BF16 or FC_DTYPE_F32 for int8 pages.
  * int8 pages: scale = max_d |x| / 127 in fp32, code = x / (max_d |x| / 127)
  * rounded to nearest, ties to even, decided exactly; an all-zero row stores

@@ -542,12 +542,16 @@ def test_captured_steps_are_replayed_after_each_begin():
             for _ in range(2))
     outs = [torch.zeros(4, 8, 1, 128, device=DEV) for _ in range(2)]
     c.begin([2], rows=4)                     # the captured launches' shape
+    saved = c.save_map()
     g = torch.cuda.CUDAGraph()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
-        with pytest.raises(FcError):         # bookkeeping is not captured
-            c.begin([2], rows=4)
+        for call in (lambda: c.begin([2], rows=4), lambda: c.free([2]),
+                     lambda: c.fork([0], [2]), c.compact, c.reset,
+                     lambda: c.crop(0, -1), lambda: c.restore_map(*saved)):
+            with pytest.raises(FcError):     # bookkeeping is not captured
+                call()
         for layer in range(2):
             c.step(q[layer], k[layer], v[layer], layer=layer, out=outs[layer])
     torch.cuda.current_stream().wait_stream(side)
@@ -569,6 +573,70 @@ def test_captured_steps_are_replayed_after_each_begin():
         for i, s in enumerate(slots):        # the tokens are part of the slot
             f.k[s] = torch.cat([f.k[s], x[1][:, i, :, 0][:, None]], 1)
             f.v[s] = torch.cat([f.v[s], x[2][:, i, :, 0][:, None]], 1)
+
+
+def test_replay_after_a_smaller_batch_leaves_the_other_slots():
+    """Rows that a smaller batch no longer has are empty for a captured step of
+    the larger one: it writes nothing to their slots."""
+    f = Filled([40, 7, 30], spare=6, seed=32)
+    c = f.cache
+    gen = torch.Generator().manual_seed(33)
+    x = [rand(gen, 3, h, 1, 128, dtype=BF).to(DEV) for h in (8, 2, 2)]
+    c.begin([0, 1, 2])
+    out = torch.zeros(3, 8, 1, 128, device=DEV)
+    c.step(*x, out=out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.step(*x, out=out)
+    c.begin([1])
+    keep = [[t.clone() for t in c.read(s)] for s in (0, 2)]
+    x[1].add_(1.0)
+    g.replay()
+    assert not out[1:].any()
+    for s, rows in zip((0, 2), keep):
+        for a, b in zip(c.read(s), rows):
+            assert torch.equal(a, b)
+    assert torch.equal(c.read(1)[0][:, :, -1], x[1][0, :, 0][None])
+
+
+def test_two_graphs_side_by_side():
+    """Graphs captured on one stream and replayed on two at once: each has a
+    workspace of its own."""
+    f = Filled([5000, 80], layers=2, page=32, seed=42)
+    gen = torch.Generator().manual_seed(43)
+    q = rand(gen, 2, 8, 1, 128, dtype=BF).to(DEV)
+    f.cache.begin([0, 1], 0)
+    want = [f.cache.attention(q, layer=i) for i in (0, 1)]
+    outs = [torch.zeros_like(w) for w in want]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g):
+            for _ in range(10):
+                f.cache.attention(q, layer=i, out=outs[i])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+@pytest.mark.parametrize("kv,Hk,G,page,D", [
+    ("bf16", 7, 16, 1024, 64), ("i8", 13, 2, 256, 128), ("f32", 1, 1, 8, 256),
+    ("i8", 3, 8, 8, 256), ("bf16", 33, 4, 64, 32)])
+def test_odd_heads_and_page_sizes(kv, Hk, G, page, D):
+    lens = [1030, 1, 15, 2047, 0, 300]
+    f = Filled(lens, kv, Hk=Hk, D=D, page=page, seed=Hk, hide=(700, 9))
+    gen = torch.Generator().manual_seed(Hk)
+    dt = F32 if kv == "f32" else BF
+    for qd in (dt, F32):
+        q = rand(gen, 6, Hk * G, 1, D, dtype=qd)
+        f.cache.begin(range(6), 0)
+        got = f.cache.attention(q.to(DEV), window=700, sinks=9)
+        check_attention(got, q, f, G, window=700, sinks=9)
 
 
 def test_other_streams_and_concurrent_calls():
