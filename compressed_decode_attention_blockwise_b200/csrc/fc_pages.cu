@@ -46,13 +46,8 @@ struct Recs {
 };
 
 // One warp per record. Records of one call never touch the same entry.
-template <int N>
-__global__ void __launch_bounds__(256) edit_map_kernel(const __grid_constant__ Recs<N> p) {
-  const int i = int(blockIdx.x) * 8 + int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
-  after_previous();
-  if (i >= p.n) return;
-  const Rec r = p.r[i];
-  const MapView& m = p.m;
+__device__ __forceinline__ void apply_record(const MapView& m, const Rec& r) {
+  const int lane = int(threadIdx.x & 31);
   switch (r.op) {
     case kRow:
       if (lane == 0) {
@@ -73,6 +68,13 @@ __global__ void __launch_bounds__(256) edit_map_kernel(const __grid_constant__ R
       if (lane == 0) m.lens[r.b] = r.d;
       break;
   }
+}
+
+template <int N>
+__global__ void __launch_bounds__(256) edit_map_kernel(const __grid_constant__ Recs<N> p) {
+  const int i = int(blockIdx.x) * 8 + int(threadIdx.x >> 5);
+  after_previous();
+  if (i < p.n) apply_record(p.m, p.r[i]);
 }
 
 template <int N>
@@ -115,26 +117,35 @@ struct CopyShape {
   int32_t first_moved;                 // entries below it stay
   unsigned copy_blocks;
 };
-template <int N>
+template <int N, int NR>
 struct Pairs {
   CopyShape s;
-  int32_t n;
+  int32_t n, n_recs;
   Pair p[N];  // ascending in src where a table is remapped
+  MapView m;
+  Rec r[NR > 0 ? NR : 1];
 };
 
 constexpr int kPieceBytes = 4096;
 
 // A warp per unit: (pair, layer, k or v, head, 4 KB piece), all its loads in
 // flight before the first store. Sources and destinations are disjoint pages.
-// The blocks past copy_blocks rewrite the table: an entry that names a moved
-// page gets the page's new place (binary search in the pairs).
-template <int N>
-__global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__ Pairs<N> a) {
+// The blocks past copy_blocks see to the map: they apply the NR records that
+// came along (a step's copies and edits in one launch), or rewrite the table,
+// where an entry that names a moved page gets the page's new place (binary
+// search in the pairs).
+template <int N, int NR>
+__global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__ Pairs<N, NR> a) {
   const CopyShape& s = a.s;
   after_previous();
   const int lane = int(threadIdx.x & 31);
+  if (NR > 0 && blockIdx.x >= s.copy_blocks) {
+    const int i = int(blockIdx.x - s.copy_blocks) * 8 + int(threadIdx.x >> 5);
+    if (i < a.n_recs) apply_record(a.m, a.r[i]);
+    return;
+  }
   if (blockIdx.x >= s.copy_blocks) {
-    __shared__ Pair sp[N];
+    __shared__ Pair sp[NR > 0 ? 1 : N];
     for (int i = int(threadIdx.x); i < a.n; i += 256) sp[i] = a.p[i];
     __syncthreads();
     const int64_t step = int64_t(gridDim.x - s.copy_blocks) * 256;
@@ -179,11 +190,18 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__
   }
 }
 
-template <int N>
-int launch_pairs(const CopyShape& shape, const Pair* pr, int n, cudaStream_t stream) {
-  Pairs<N> a;
+template <int N, int NR>
+int launch_pairs(const CopyShape& shape, const Pair* pr, int n, const MapView& m, const std::vector<Rec>* recs,
+                 cudaStream_t stream) {
+  Pairs<N, NR> a;
   a.s = shape;
   a.n = n;
+  a.n_recs = 0;
+  if (NR > 0) {
+    a.m = m;
+    a.n_recs = int32_t(recs->size());
+    for (int i = 0; i < a.n_recs; ++i) a.r[i] = (*recs)[size_t(i)];
+  }
   for (int i = 0; i < n; ++i) a.p[i] = pr[i];
   a.s.row_units = uint32_t(n) * shape.n_layers * 2 * shape.H * shape.pieces;
   a.s.all_units = a.s.row_units + (shape.base[2] ? uint32_t(n) * shape.n_layers * 2 * shape.H : 0);
@@ -191,15 +209,20 @@ int launch_pairs(const CopyShape& shape, const Pair* pr, int n, cudaStream_t str
   int64_t blocks = (int64_t(a.s.all_units) + 7) / 8;
   if (blocks > most) blocks = most;
   a.s.copy_blocks = unsigned(blocks);
+  blocks += (a.n_recs + 7) / 8;
   if (shape.table) {
     int64_t t = (shape.table_entries + 1023) / 1024;
     blocks += t > 64 ? 64 : t;
     a.s.first_moved = pr[0].src;
   }
-  return launch_after(copy_pages_kernel<N>, dim3(unsigned(blocks)), 256, 0, stream, a);
+  return launch_after(copy_pages_kernel<N, NR>, dim3(unsigned(blocks)), 256, 0, stream, a);
 }
 
-int launch_copies(const fc_pages* p, const std::vector<Pair>& pairs, bool remap, cudaStream_t stream) {
+// Copies the pairs' pages; remap: rewrites the table by them; recs (or null):
+// edits of the map that go along.
+int launch_copies(const fc_pages* p, const std::vector<Pair>& pairs, bool remap, const std::vector<Rec>* recs,
+                  cudaStream_t stream) {
+  const MapView m{p->table, p->lens, p->batch, p->max_pages};
   CopyShape s{};
   const int64_t es = dtype_size(p->dtype);
   s.base[0] = static_cast<char*>(p->k);
@@ -226,15 +249,18 @@ int launch_copies(const fc_pages* p, const std::vector<Pair>& pairs, bool remap,
     s.table = p->table;
     s.table_entries = p->n_slots * p->max_pages;
   }
+  if (recs && !pairs.empty() && pairs.size() <= size_t(kFewPairs) && pairs.size() <= most &&
+      recs->size() <= size_t(kFewRecs))
+    return launch_pairs<kFewPairs, kFewRecs>(s, pairs.data(), int(pairs.size()), m, recs, stream);
   for (size_t at = 0; at < pairs.size();) {
     const size_t left = pairs.size() - at;
     const int n = int(left > most ? most : left);
-    const int st = n <= kFewPairs ? launch_pairs<kFewPairs>(s, &pairs[at], n, stream)
-                                  : launch_pairs<kManyPairs>(s, &pairs[at], n, stream);
+    const int st = n <= kFewPairs ? launch_pairs<kFewPairs, 0>(s, &pairs[at], n, m, nullptr, stream)
+                                  : launch_pairs<kManyPairs, 0>(s, &pairs[at], n, m, nullptr, stream);
     if (st != FC_OK) return st;
     at += size_t(n);
   }
-  return FC_OK;
+  return recs ? launch_edits(p, *recs, stream) : FC_OK;
 }
 
 // ----------------------------------------------------- uploading a whole map
@@ -567,8 +593,7 @@ extern "C" int fc_pages_begin(fc_pages* p, const int32_t* slots, const int32_t* 
     p->n_tokens = total;
     p->one_each = one_each ? 1 : 0;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if ((st = launch_copies(p, copies, false, cs)) != FC_OK) return st;
-    if ((st = launch_edits(p, recs, cs)) != FC_OK) return st;
+    if ((st = launch_copies(p, copies, false, &recs, cs)) != FC_OK) return st;
     ed.keep();
     return FC_OK;
   });
@@ -657,7 +682,7 @@ extern "C" int fc_pages_compact(fc_pages* p, int64_t* n_live, fc_stream stream) 
     if (!moves.empty()) {
       std::vector<int32_t> to(size_t(p->n_pages - live), -1);
       for (const Pair& m : moves) to[size_t(m.src - live)] = m.dst;
-      const int st = launch_copies(p, moves, true, static_cast<cudaStream_t>(stream));
+      const int st = launch_copies(p, moves, true, nullptr, static_cast<cudaStream_t>(stream));
       if (st != FC_OK) return st;
       for (int64_t s = 0; s < p->n_slots; ++s) {
         int32_t* row = p->h_table + s * p->max_pages;
