@@ -8,7 +8,6 @@ missing library is an error, never a fallback.
 
 from __future__ import annotations
 
-import array
 import ctypes
 import os
 from typing import Optional
@@ -612,16 +611,6 @@ def fc_select_batch(src: FcArchive, src_tail: Optional[FcTail], idx,
 
 # ------------------------------------------------------------- paged cache
 
-class _Ints:
-    """A host int32 array of a list (array.array converts several times
-    faster than a ctypes array does)."""
-    __slots__ = ("a", "p")
-
-    def __init__(self, values):
-        self.a = None if values is None else array.array("i", values)
-        self.p = None if values is None else self.a.buffer_info()[0]
-
-
 def fc_pages_reset(pages: FcPages, stream: int) -> None:
     _check(load().fc_pages_reset(pages, stream), "fc_pages_reset")
 
@@ -630,25 +619,6 @@ def fc_pages_restore(pages: FcPages, table: torch.Tensor, lens: torch.Tensor,
                      stream: int) -> None:
     _check(load().fc_pages_restore(pages, table.data_ptr(), lens.data_ptr(),
                                    stream), "fc_pages_restore")
-
-
-def fc_pages_begin(pages: FcPages, slots, counts, n_rows: int,
-                   stream: int) -> None:
-    s, c = _Ints(slots), _Ints(counts)
-    _check(load().fc_pages_begin(pages, s.p, c.p, len(slots), n_rows, stream),
-           "fc_pages_begin")
-
-
-def fc_pages_fork(pages: FcPages, src, dst, stream: int) -> None:
-    s, d = _Ints(src), _Ints(dst)
-    _check(load().fc_pages_fork(pages, s.p, d.p, len(dst), stream),
-           "fc_pages_fork")
-
-
-def fc_pages_free(pages: FcPages, slots, stream: int) -> None:
-    s = _Ints(slots)
-    _check(load().fc_pages_free(pages, s.p, len(slots), stream),
-           "fc_pages_free")
 
 
 def fc_pages_crop(pages: FcPages, slot: int, tokens_to_remove: int,

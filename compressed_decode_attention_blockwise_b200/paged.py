@@ -15,6 +15,7 @@ decisions and every byte of arithmetic are libfc's.
 
 from __future__ import annotations
 
+import array
 import ctypes
 from typing import Optional
 
@@ -75,7 +76,9 @@ class PagedKVCache:
         self._h_table = torch.full((n_slots, self.max_pages), -1, **i32)
         self._h_lens = torch.zeros(n_slots, **i32)
         self._h_refs = torch.zeros(n_pages, **i32)
-        self._np_lens = self._h_lens.numpy()
+        # (indexed without a tensor's cost)
+        self._len_of = (ctypes.c_int32 * n_slots).from_address(
+            self._h_lens.data_ptr())
         p = self.pages = _lib.FcPages()
         p.k, p.v = self.k.data_ptr(), self.v.data_ptr()
         if self.k_scales is not None:
@@ -94,6 +97,7 @@ class PagedKVCache:
         self._lib = _lib.load()
         self._ref = ctypes.byref(p)
         self._index = -1 if device.type != "cuda" else device.index
+        self._where = device if self._index < 0 else self._index
         self._rows = 0             # rows of the open batch (0: none)
         self._ws: dict = {}        # (stream, Hq) -> workspace
         self._dense: dict = {}     # Hq -> strides of a fresh output
@@ -145,16 +149,21 @@ class PagedKVCache:
         Raises FcError with FC_ERR_CAPACITY, nothing changed, when the pages
         do not suffice."""
         slots = _ints(slots)
+        n = len(slots)
         if isinstance(counts, int):
-            counts = [counts] * len(slots)
+            counts = array.array("i", [counts]) * n
         elif counts is not None:
             counts = _ints(counts)
-            if len(counts) != len(slots):
+            if len(counts) != n:
                 raise ValueError("one count per slot")
+        rows = rows or n
         with self._on_device():
-            _lib.fc_pages_begin(self.pages, slots, counts,
-                                rows or len(slots), self._stream())
-        self._rows = rows or len(slots)
+            st = self._lib.fc_pages_begin(
+                self._ref, slots.buffer_info()[0], None if counts is None
+                else counts.buffer_info()[0], n, rows, self._stream())
+        if st:
+            raise _lib.FcError(st, "fc_pages_begin")
+        self._rows = rows
 
     def fork(self, src, dst):
         """Slot ``dst[i]`` (empty) shares the pages of ``src[i]``."""
@@ -162,13 +171,21 @@ class PagedKVCache:
         if len(src) != len(dst):
             raise ValueError("one source per destination")
         with self._on_device():
-            _lib.fc_pages_fork(self.pages, src, dst, self._stream())
+            st = self._lib.fc_pages_fork(
+                self._ref, src.buffer_info()[0], dst.buffer_info()[0],
+                len(dst), self._stream())
+        if st:
+            raise _lib.FcError(st, "fc_pages_fork")
         self._rows = 0
 
     def free(self, slots):
         """Empty the slots; pages no other slot shares become free."""
+        slots = _ints(slots)
         with self._on_device():
-            _lib.fc_pages_free(self.pages, _ints(slots), self._stream())
+            st = self._lib.fc_pages_free(
+                self._ref, slots.buffer_info()[0], len(slots), self._stream())
+        if st:
+            raise _lib.FcError(st, "fc_pages_free")
         self._rows = 0
 
     def crop(self, slot: int, tokens_to_remove: int):
@@ -206,7 +223,7 @@ class PagedKVCache:
         self._rows = 0
 
     def seq_len(self, slot: int) -> int:
-        return int(self._np_lens[slot])
+        return self._len_of[slot]
 
     @property
     def free_pages(self) -> int:
@@ -364,8 +381,8 @@ class PagedKVCache:
         if code is None:
             raise ValueError("rows are read as bfloat16 or float32")
         T = self.seq_len(slot)
-        k, v = torch.empty((2, 1, self.Hk, T, self.D), dtype=dt,
-                           device=self.device).unbind(0)
+        k, v = torch.empty(2, 1, self.Hk, T, self.D, dtype=dt,
+                           device=self._where).unbind(0)
         strides = _I64x4(self.Hk * T * self.D, T * self.D, self.D, 1)
         with self._on_device():
             st = self._lib.fc_paged_read(
@@ -388,8 +405,8 @@ _NO_GUARD = _NoGuard()
 
 
 def _ints(x):
+    """A host int32 array of the integers in x (array.array converts several
+    times faster than a ctypes array does)."""
     if isinstance(x, torch.Tensor):
         x = x.tolist()
-    if type(x) is not list:
-        x = list(x)
-    return x
+    return array.array("i", x)
