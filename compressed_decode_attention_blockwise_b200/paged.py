@@ -100,7 +100,7 @@ class PagedKVCache:
         self._where = device if self._index < 0 else self._index
         self._rows = 0             # rows of the open batch (0: none)
         self._ws: dict = {}        # (stream, Hq) -> workspace
-        self._dense: dict = {}     # Hq -> strides of a fresh output
+        self._dense: dict = {}     # H -> strides of a dense (rows, H, 1, D)
         self.reset()
 
     def _check_storage(self, shape, store):
@@ -260,17 +260,12 @@ class PagedKVCache:
         if st:
             raise _lib.FcError(st, "fc_paged_append")
 
-    def _workspace(self, Hq: int, stream: int):
-        """(tensor, address, bytes) of this stream's workspace."""
-        if self._index >= 0 and torch._C._cuda_isCurrentStreamCapturing():
-            # a graph's own: graphs may be replayed side by side
-            return self._new_workspace(Hq)
-        ws = self._ws.get((stream, Hq))
-        if ws is None:
-            ws = self._ws[stream, Hq] = self._new_workspace(Hq)
-        return ws
+    def _dense_strides(self, H: int):
+        d = self._dense[H] = _I64x4(H * self.D, self.D, self.D, 1)
+        return d
 
     def _new_workspace(self, Hq: int):
+        """(tensor, address, bytes) of a zeroed workspace."""
         n = _lib.fc_paged_workspace_bytes(Hq, self.Hk, self.D)
         if n == 0:
             raise _lib.FcError(_lib.FC_ERR_UNSUPPORTED,
@@ -294,13 +289,11 @@ class PagedKVCache:
                 q.get_device() != self._index:
             self._refuse_query(q)
         Hq = shape[1]
+        dense = self._dense.get(Hq) or self._dense_strides(Hq)
         if out is None:
             out = torch.empty_like(q, dtype=out_dtype,
                                    memory_format=torch.contiguous_format)
-            strides = self._dense.get(Hq)
-            if strides is None:
-                strides = self._dense[Hq] = _I64x4(Hq * self.D, self.D,
-                                                   self.D, 1)
+            strides = dense
         else:
             out_dtype = out.dtype
             if out.shape != shape or out.get_device() != self._index:
@@ -310,34 +303,45 @@ class PagedKVCache:
         out_code = _FLOAT.get(out_dtype)
         if out_code is None:
             raise ValueError("out must be bfloat16 or float32")
-        if lse is not None and (lse.shape != shape[:2] or
-                                lse.dtype != torch.float32 or
-                                lse.get_device() != self._index or
-                                not lse.is_contiguous()):
-            raise ValueError("lse must be a contiguous float32 (rows, Hq) "
-                             "tensor on %s" % self.device)
-        guard = self._on_device()
-        guard.__enter__()
-        try:
-            s = self._stream()
-            _, ws, ws_bytes = self._workspace(Hq, s)
-            scale = 0.0 if softmax_scale is None else softmax_scale
-            lse_ptr = None if lse is None else lse.data_ptr()
-            if new is None:
-                st = self._lib.fc_paged_attention(
-                    self._ref, layer, q.data_ptr(), code, _I64x4(*q.stride()),
-                    Hq, scale, window, sinks, ws, ws_bytes, out.data_ptr(),
-                    out_code, strides, lse_ptr, s)
-            else:
-                k, v = new
-                st = self._lib.fc_paged_step(
-                    self._ref, layer, q.data_ptr(), code, _I64x4(*q.stride()),
-                    Hq, k.data_ptr(), v.data_ptr(), _FLOAT[k.dtype],
-                    _I64x4(*k.stride()), _I64x4(*v.stride()), scale, window,
-                    sinks, ws, ws_bytes, out.data_ptr(), out_code, strides,
-                    lse_ptr, s)
-        finally:
-            guard.__exit__(None, None, None)
+        lse_ptr = None
+        if lse is not None:
+            if lse.shape != shape[:2] or lse.dtype != torch.float32 or \
+                    lse.get_device() != self._index or \
+                    not lse.is_contiguous():
+                raise ValueError("lse must be a contiguous float32 (rows, Hq) "
+                                 "tensor on %s" % self.device)
+            lse_ptr = lse.data_ptr()
+        if self._index >= 0 and torch._C._cuda_getDevice() != self._index:
+            with torch.cuda.device(self.device):
+                return self._attend(q, new, layer, out, softmax_scale, window,
+                                    sinks, out_dtype, lse)
+        s = self._stream()
+        if self._index >= 0 and torch._C._cuda_isCurrentStreamCapturing():
+            # a graph's own: graphs may be replayed side by side
+            ws = self._new_workspace(Hq)
+        else:
+            ws = self._ws.get((s, Hq))
+            if ws is None:
+                ws = self._ws[s, Hq] = self._new_workspace(Hq)
+        if softmax_scale is None:
+            softmax_scale = 0.0
+        qs = dense if q.is_contiguous() else _I64x4(*q.stride())
+        if new is None:
+            st = self._lib.fc_paged_attention(
+                self._ref, layer, q.data_ptr(), code, qs, Hq, softmax_scale,
+                window, sinks, ws[1], ws[2], out.data_ptr(), out_code,
+                strides, lse_ptr, s)
+        else:
+            k, v = new
+            new_dense = self._dense.get(self.Hk) or \
+                self._dense_strides(self.Hk)
+            st = self._lib.fc_paged_step(
+                self._ref, layer, q.data_ptr(), code, qs, Hq, k.data_ptr(),
+                v.data_ptr(), _FLOAT[k.dtype],
+                new_dense if k.is_contiguous() else _I64x4(*k.stride()),
+                new_dense if v.is_contiguous() else _I64x4(*v.stride()),
+                softmax_scale, window, sinks, ws[1], ws[2], out.data_ptr(),
+                out_code, strides, lse_ptr, s)
         if st:
             raise _lib.FcError(st, "fc_paged_attention" if new is None else
                                "fc_paged_step")
