@@ -134,15 +134,23 @@ __global__ void __launch_bounds__(kAppendThreads) append_i8_kernel(const __grid_
       load_token_row<E>(s.p, (kv ? at.v : at.k)[tok] + h * s.sh, a.dtype, a.vec, x[u], lane);
     }
     if (base == 0) at.places(a, n0, a.ahead);
-#pragma unroll
+    // one copy of the quantiser's code: a short launch waits for its code first
+#pragma unroll 1
     for (int u = 0; u < kRows; ++u) {
+      float y[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        y[i] = x[0][i];
+#pragma unroll
+        for (int k = 1; k < kRows; ++k) x[k - 1][i] = x[k][i];
+      }
       const int row = base + u * W + warp, tok = row / (2 * H), kv = row / H & 1, h = row % H;
       if (row >= rows || at.page[tok] < 0) continue;
       int8_t* d = reinterpret_cast<int8_t*>(kv ? a.pages.v : a.pages.k) + at.page[tok] * a.pages.stride_page +
                   h * a.pages.stride_head + int64_t(at.in[tok]) * D;
       float* sc = (kv ? a.pages.vs : a.pages.ks) + at.page[tok] * a.pages.sstride_page +
                   h * a.pages.sstride_head + at.in[tok];
-      quantise_row<E>(x[u], d + lane * E, sc, lane);
+      quantise_row<E>(y, d + lane * E, sc, lane);
     }
   }
 }
@@ -155,31 +163,31 @@ struct ReadArgs {
   int32_t slot, len;
 };
 
-// Dense rows of one slot, 16-byte loads or stores, kAhead rows in flight per
+// Dense rows of one slot, 16-byte loads or stores, AHEAD rows in flight per
 // thread; bound by HBM (pages read + rows written). Rows that keep their type
 // are moved as they are.
-template <typename T, typename TO, int D>
+template <typename T, typename TO, int D, int AHEAD>
 __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr bool kMove = std::is_same<T, TO>::value;
   constexpr int E = kMove ? 16 / int(sizeof(T)) : 8;  // elements per thread and row
   constexpr int V = D / E, kRows = 256 / V;
   const int group = int(threadIdx.x) / V, w = int(threadIdx.x) % V;
   const int h = int(blockIdx.y) >> 1, kv = int(blockIdx.y) & 1;
-  const int32_t t0 = int32_t(blockIdx.x) * (kAhead * kRows) + group;
+  const int32_t t0 = int32_t(blockIdx.x) * (AHEAD * kRows) + group;
   const T* const pool = reinterpret_cast<const T*>(kv ? a.pages.v : a.pages.k) + h * a.pages.stride_head + w * E;
   TO* const out = static_cast<TO*>(kv ? a.v : a.k) + h * (kv ? a.vs_h : a.ks_h) + w * E;
   const int64_t os = kv ? a.vs_t : a.ks_t;
-  int32_t page[kAhead];
+  int32_t page[AHEAD];
   after_previous();
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
+  for (int u = 0; u < AHEAD; ++u) {
     const int32_t t = t0 + u * kRows;
     page[u] = t < a.len ? page_of(a.pages, a.slot, t) : -1;
   }
-  uint4 x[kAhead];
-  float f[kAhead][kMove ? 1 : E];
+  uint4 x[AHEAD];
+  float f[AHEAD][kMove ? 1 : E];
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
+  for (int u = 0; u < AHEAD; ++u) {
     if (page[u] < 0) continue;
     const int32_t in = (t0 + u * kRows) & ((1 << a.pages.log2P) - 1);
     const T* p = pool + page[u] * a.pages.stride_page + int64_t(in) * D;
@@ -195,7 +203,7 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__
     }
   }
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
+  for (int u = 0; u < AHEAD; ++u) {
     if (page[u] < 0) continue;
     TO* o = out + (t0 + u * kRows) * os;
     if constexpr (kMove) {
@@ -210,11 +218,11 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__
   }
 }
 
-// Tokens per thread: eight, or two while the CTAs of eight would not fill the
-// GPU (a launch of few tokens is all latency).
+// Tokens per thread: eight, or two or one while the CTAs of more would not fill
+// the GPU (a launch of few tokens is all latency).
 template <int D>
 int launch_append(AppendArgs a, int pages_dtype, cudaStream_t s) {
-  a.ahead = a.offered < int64_t(sm_count()) * 32 ? 2 : kAhead;
+  a.ahead = a.offered < int64_t(sm_count()) * 8 ? 1 : a.offered < int64_t(sm_count()) * 32 ? 2 : kAhead;
   a.side = 1;
   if (pages_dtype != FC_DTYPE_I8) {
     const int words = 2 * a.pages.H * (D * dtype_size(pages_dtype) / 16);
@@ -232,9 +240,13 @@ int launch_append(AppendArgs a, int pages_dtype, cudaStream_t s) {
 template <typename T, typename TO, int D>
 int launch_read_as(const ReadArgs& a, cudaStream_t s) {
   constexpr int E = std::is_same<T, TO>::value ? 16 / int(sizeof(T)) : 8;
-  constexpr unsigned kTile = kAhead * 256 / (D / E);
-  const dim3 grid((unsigned(a.len) + kTile - 1) / kTile, unsigned(a.pages.H) * 2);
-  return launch_after(paged_read_kernel<T, TO, D>, grid, 256, 0, s, a);
+  constexpr unsigned kRows = 256 / (D / E);  // rows of a CTA in one pass
+  const unsigned heads = unsigned(a.pages.H) * 2, len = unsigned(a.len);
+  // eight rows per thread, or one while the CTAs of eight would not fill the GPU
+  if (int64_t(len) * heads < int64_t(sm_count()) * 2 * kAhead * kRows)
+    return launch_after(paged_read_kernel<T, TO, D, 1>, dim3((len + kRows - 1) / kRows, heads), 256, 0, s, a);
+  constexpr unsigned kTile = kAhead * kRows;
+  return launch_after(paged_read_kernel<T, TO, D, kAhead>, dim3((len + kTile - 1) / kTile, heads), 256, 0, s, a);
 }
 template <typename T, int D>
 int launch_read(const ReadArgs& a, int out_dtype, cudaStream_t s) {

@@ -385,8 +385,8 @@ class PagedKVCache:
         if code is None:
             raise ValueError("rows are read as bfloat16 or float32")
         T = self.seq_len(slot)
-        k, v = torch.empty(2, 1, self.Hk, T, self.D, dtype=dt,
-                           device=self._where).unbind(0)
+        k = torch.empty(1, self.Hk, T, self.D, dtype=dt, device=self._where)
+        v = torch.empty_like(k)
         strides = _I64x4(self.Hk * T * self.D, T * self.D, self.D, 1)
         with self._on_device():
             st = self._lib.fc_paged_read(
