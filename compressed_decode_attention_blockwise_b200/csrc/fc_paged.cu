@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__
     if constexpr (kMove) {
       x[u] = __ldcs(reinterpret_cast<const uint4*>(p));
     } else {
-      load_vec<T, E>(p, f[u]);
+      load_elems<T, E>(p, f[u]);
       if constexpr (sizeof(T) == 1) {
         const float s = (kv ? a.pages.vs : a.pages.ks)[page[u] * a.pages.sstride_page + h * a.pages.sstride_head + in];
 #pragma unroll

@@ -97,6 +97,35 @@ __device__ __forceinline__ void load_words(uint32_t* w, const void* p) {
   }
 }
 
+// VEC consecutive elements as floats, by vector loads where p is aligned to
+// them. Coherent loads here and below: what a kernel reads may have been written
+// after its launch, before after_previous() returned.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_elems(const T* p, float (&out)[VEC]) {
+  constexpr int kBytes = VEC * int(sizeof(T)), kStep = kBytes < 16 ? kBytes : 16, kPerWord = 4 / int(sizeof(T));
+  if constexpr (kBytes >= 4) {
+#pragma unroll
+    for (int i = 0; i < kBytes / kStep; ++i) {
+      uint32_t w[kStep / 4];
+      load_words<kStep>(w, reinterpret_cast<const char*>(p) + i * kStep);
+#pragma unroll
+      for (int k = 0; k < kStep / 4; ++k) unpack_word<T>(w[k], &out[(i * (kStep / 4) + k) * kPerWord]);
+    }
+  } else {
+    static_assert(kBytes == 2 && VEC == 1, "one bf16");
+    unsigned short h;
+    asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(h) : "l"(p));
+    out[0] = __uint_as_float(uint32_t(h) << 16);
+  }
+}
+// One element of a runtime dtype.
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype) {
+  float x[1];
+  if (dtype == FC_DTYPE_F32) load_elems<float, 1>(static_cast<const float*>(p) + i, x);
+  else load_elems<__nv_bfloat16, 1>(static_cast<const __nv_bfloat16*>(p) + i, x);
+  return x[0];
+}
+
 // int8: code = x / (absmax / 127) to nearest, ties to even. y = |x| (127 / absmax)
 // in fp32 decides it unless y lies within 2^-12 of a half-integer (its error is
 // below 127 * 2^-22); there the exact comparison of 254 |x| with
@@ -156,12 +185,12 @@ template <int E>
 __device__ __forceinline__ void load_token_row(const void* src, int64_t elem, int src_dtype, bool vec,
                                                float (&x)[E], int lane) {
   if (vec && src_dtype == FC_DTYPE_BF16) {
-    load_vec<__nv_bfloat16, E>(static_cast<const __nv_bfloat16*>(src) + elem + lane * E, x);
+    load_elems<__nv_bfloat16, E>(static_cast<const __nv_bfloat16*>(src) + elem + lane * E, x);
   } else if (vec) {
-    load_vec<float, E>(static_cast<const float*>(src) + elem + lane * E, x);
+    load_elems<float, E>(static_cast<const float*>(src) + elem + lane * E, x);
   } else {
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = load_any(src, elem + lane * E + i, src_dtype);
+    for (int i = 0; i < E; ++i) x[i] = load_elem(src, elem + lane * E + i, src_dtype);
   }
 }
 

@@ -5,11 +5,11 @@
 // for the G query heads that share the kv head.
 //
 // What bounds it: HBM. Every seen K and V row is read once per kv head and
-// serves its whole group; at G = 8 and bf16 that is 8 multiply-adds per byte,
-// above what CUDA-core FMAs sustain at full bandwidth and a small share of the
-// tensor cores' rate. So both products run as mma.sync m16n8k16 (bf16 in, fp32
-// out) with the TOKENS (and for V the channels) on the 16-wide side and the
-// heads on the 8-wide one:
+// serves its whole group; at G = 8 and bf16 that is four multiply-adds per byte
+// and a conversion per element, most of what the CUDA cores can do at full
+// bandwidth and little of what the tensor cores can (12 % busy). So both
+// products run as mma.sync m16n8k16 (fp32 out) with the TOKENS (and for V the
+// channels) on the 16-wide side and the heads on the 8-wide one:
 //   S^T (16 tokens x 8 heads)  = K (16 x D) . Q^T,
 //   O^T (16 channels x 8 heads) += V^T (16 x 16 tokens) . P^T.
 // A 128-row tcgen05 tile would have to be gathered from several pages into
@@ -28,7 +28,14 @@
 // which takes fewer instructions than bf16 and holds 11 bits a limb: the query
 // (brought to fp16's range by a power of two per head) is one limb, two when
 // it is fp32, and P times V's scale (by a power of two per warp) is two.
-// Maxima, sums and accumulators are fp32.
+// Maxima, sums and accumulators are fp32. Against 64 bits: 1e-6 of the output at
+// most in fp32, the output's own rounding in bf16.
+//
+// Measured (B200, calls back to back): one bf16 sequence of 131,075 tokens, 32
+// query and 8 kv heads of 128: 91 us, 5.9 TB/s, 0.90 of the copy rate. 64 int8
+// sequences of up to 8,199 tokens, 64 / 8 heads: 167 us, 4.2 TB/s, bound by its
+// 467 instructions per tile. One fp32 sequence of 256 tokens, 4 heads of 64:
+// 9.5 us, all latency.
 //
 // Softmax: each warp keeps its own running maximum per head and raises it only
 // when a tile exceeds it by more than 2^8 (a vote); until then p <= 2^8 and the
@@ -288,8 +295,8 @@ struct Piece {
 
 // Four query elements at q[at ..], of either type and any alignment.
 static __device__ __noinline__ float4 load_query_slow(const void* q, int64_t at, int dtype) {
-  return make_float4(load_any(q, at, dtype), load_any(q, at + 1, dtype), load_any(q, at + 2, dtype),
-                     load_any(q, at + 3, dtype));
+  return make_float4(load_elem(q, at, dtype), load_elem(q, at + 1, dtype), load_elem(q, at + 2, dtype),
+                     load_elem(q, at + 3, dtype));
 }
 
 // The new token's K and V rows of a kv head, to their page.
@@ -474,7 +481,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
         for (int i = 0; i < D / 32; ++i) {
           w[i] = make_uint4(0, 0, 0, 0);
           if (g < a.G)
-            w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + qh + i * 32 + c * 8));
+            load_words<16>(&w[i].x, static_cast<const __nv_bfloat16*>(a.q.p) + qh + i * 32 + c * 8);
         }
         if (nt == 0) fetch(held, cur);  // the table's latency with the query's
 #pragma unroll
@@ -493,9 +500,9 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
               const float4 z = load_query_slow(a.q.p, qh + d, a.q_dtype);
               y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
             } else if (QL == 1 || a.q_dtype != FC_DTYPE_F32) {
-              load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16*>(a.q.p) + qh + d, y);
+              load_elems<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16*>(a.q.p) + qh + d, y);
             } else {
-              load_vec<float, 4>(static_cast<const float*>(a.q.p) + qh + d, y);
+              load_elems<float, 4>(static_cast<const float*>(a.q.p) + qh + d, y);
             }
           }
 #pragma unroll
