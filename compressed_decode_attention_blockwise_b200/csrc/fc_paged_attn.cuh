@@ -108,9 +108,11 @@ struct PagedCfg {
   // tiles per iteration: more than one only where a tile is a few loads (two for
   // int8 rows of 128 spilled: 250 us against 195 for 64 sequences of 8K)
   static constexpr int U = KW >= 8 ? 1 : 2;
-  // rows too wide for the registers are taken in parts, without prefetch
+  // Rows too wide for the registers are taken in parts (two, or four), and only
+  // the first part of K and of V is loaded ahead. fp32 rows need room for their
+  // limbs besides (16 heads of 128: 2.6 TB/s whole, 3.2 in two parts).
   static constexpr int kRegs = NT * D / 4 + U * (2 * KW + 4 * VW);
-  static constexpr int CH = kRegs <= 192 ? 1 : kRegs <= 256 ? 2 : 4;
+  static constexpr int CH = kRegs <= (ES == 4 ? 160 : 192) ? 1 : NT * D / 4 + 2 * U * KW <= (ES == 4 ? 176 : 192) ? 2 : 4;
   static constexpr bool kPrefetch = CH == 1;
   static constexpr int NQ = NT * D / 16;      // float4 accumulators per lane
   static constexpr int WARPS = NQ >= 32 ? 4 : NQ >= 16 || kRegs > 96 ? 8 : kRegs > 48 || NT > 1 ? 12 : 16;
@@ -651,20 +653,22 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
         });
     };
 
+    if constexpr (!C::kPrefetch) {
+      advance(tile);
+      load_k(tile, 0);
+    }
     // The first pass only loads (the loads' code is there once).
 #pragma unroll 1
     for (int32_t i = C::kPrefetch ? tile - U : tile; i < end; i += U) {
       const bool work = !C::kPrefetch || i >= tile;
       float s[U][NT][4];
-      if constexpr (!C::kPrefetch) {
-        advance(i);
-      }
+      if constexpr (!C::kPrefetch) load_v(i, 0);
       if (work) {
         // ---- S^T = K Q^T
         float odd[U][NT][4];  // a second chain of dependent products
 #pragma unroll
         for (int part = 0; part < CH; ++part) {
-          if constexpr (!C::kPrefetch) load_k(i, part);
+          if (part > 0) load_k(i, part);
           constexpr int STEPS = D / 16 / CH;  // k-steps of 16 channels per part
           static_assert(STEPS % 2 == 0, "two chains");
           uint4 qb[QL][NT];  // the query's words of two k-steps
@@ -833,7 +837,11 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
         // own, added in fp32 (the tensor cores' running sums are truncated)
 #pragma unroll
         for (int part = 0; part < CH; ++part) {
-          if constexpr (!C::kPrefetch) load_v(i, part);
+          if (part > 0) load_v(i, part);
+          if (!C::kPrefetch && part == CH - 1) {
+            advance(i + U);
+            load_k(i + U, 0);
+          }
 #pragma unroll
           for (int mt = 0; mt < MT / CH; ++mt) {
             float o[NT][4];
