@@ -109,10 +109,11 @@ struct PagedCfg {
   // int8 rows of 128 spilled: 250 us against 195 for 64 sequences of 8K)
   static constexpr int U = KW >= 8 ? 1 : 2;
   // Rows too wide for the registers are taken in parts (two, or four), and only
-  // the first part of K and of V is loaded ahead. fp32 rows need room for their
-  // limbs besides (16 heads of 128: 2.6 TB/s whole, 3.2 in two parts).
+  // the first part of K and of V is loaded ahead. fp32 and int8 rows need room
+  // for their limbs and conversions besides (16 heads of 128 in fp32: 2.6 TB/s
+  // whole, 3.4 in two parts; 16 of 256 in int8: 1.5 and 1.6).
   static constexpr int kRegs = NT * D / 4 + U * (2 * KW + 4 * VW);
-  static constexpr int CH = kRegs <= (ES == 4 ? 160 : 192) ? 1 : NT * D / 4 + 2 * U * KW <= (ES == 4 ? 176 : 192) ? 2 : 4;
+  static constexpr int CH = kRegs <= (ES == 2 ? 192 : 160) ? 1 : NT * D / 4 + 2 * U * KW <= (ES == 4 ? 176 : 192) ? 2 : 4;
   static constexpr bool kPrefetch = CH == 1;
   static constexpr int NQ = NT * D / 16;      // float4 accumulators per lane
   static constexpr int WARPS = NQ >= 32 ? 4 : NQ >= 16 || kRegs > 96 ? 8 : kRegs > 48 || NT > 1 ? 12 : 16;
