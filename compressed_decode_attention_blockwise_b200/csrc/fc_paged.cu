@@ -369,7 +369,8 @@ extern "C" int fc_paged_append(const fc_pages* p, int64_t layer, const void* k, 
   if (p->n_rows < 1 || p->n_rows > p->n_slots || B < 0 || M < 0 || !token_dtype_ok(p, dtype))
     return FC_ERR_INVALID;
   if ((M > 0 && B > INT_MAX / M) || B * M < p->n_tokens) return FC_ERR_INVALID;
-  if (p->n_tokens == 0) return FC_OK;
+  // nothing to write; a captured launch is there for later batches
+  if (B * M == 0 || (p->n_tokens == 0 && check_not_capturing(stream) == FC_OK)) return FC_OK;
   if (!k || !v || !k_strides || !v_strides || k_strides[3] != 1 || v_strides[3] != 1) return FC_ERR_INVALID;
   const int64_t es = dtype_size(dtype);
   if (reinterpret_cast<uintptr_t>(k) % uintptr_t(es) || reinterpret_cast<uintptr_t>(v) % uintptr_t(es))
