@@ -19,13 +19,16 @@ struct AppendArgs {
   int32_t ahead, side;   // tokens per thread and CTA: see the kernels
 };
 
-// The page row of new token n of the open batch, in rows of D elements from
-// the pool's head 0 (-1: none). Rows are found by their first token.
+// The page and the row in it of new token n of the open batch (false: none).
+// Rows are found by their first token. Empty rows, which a captured launch of
+// more rows than the open batch has finds behind the others, hold no first
+// token that the search could go by (an earlier batch's, or -1 after a reset).
 __device__ __forceinline__ bool locate_token(const PageView& p, int64_t n, int32_t* page, int32_t* in) {
-  int lo = 0, hi = p.n_rows;  // the last row with first <= n
+  int lo = 0, hi = p.n_rows;  // the last row in use with first <= n
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (p.batch[mid].first <= n) lo = mid;
+    const int4 b = reinterpret_cast<const int4*>(p.batch)[mid];  // slot, length, first, count
+    if (b.x >= 0 && b.z <= n) lo = mid;
     else hi = mid;
   }
   const BatchRow b = p.batch[lo];

@@ -57,3 +57,59 @@ def test_append_captured_over_a_batch_without_tokens(kv):
     c.begin([1, 0], [4, 2])
     g.replay()
     check_rows(c, {1: [y[:4] for y in x], 0: [y[4:] for y in x]}, kv)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+@pytest.mark.parametrize("rows,M,batches", [
+    # batches that shrink and grow again, one token a row
+    (8, 1, [[1] * 8, [1] * 2, [1] * 4, [1] * 8, [1]]),
+    # more tokens in fewer rows than an earlier batch had
+    (4, 4, [[4] * 4, [1], [16], [3, 0, 9], [0, 0, 1]]),
+    # rows as they are after a reset, and after the first batch behind it
+    (4, 1, [[1] * 4, None, [1] * 2, [1] * 3]),
+    (6, 5, [[5, 0, 2], None, [7, 11], [1] * 6, None, [1, 29]]),
+])
+def test_captured_append_writes_every_token(kv, rows, M, batches):
+    """An append captured over ``rows`` rows and rows * M tokens, replayed
+    after each begin (None: a reset) of at most as many: each new token is in
+    its page, and nothing else has been written."""
+    Hk, D, P = 2, 64, 8
+    c = PagedKVCache(1, rows, 40, Hk, D, page_size=P, max_pages=8, kv=kv,
+                     device=DEV)
+
+    def clear():
+        for pool in (c.k, c.v):
+            pool.fill_(77 if kv == "i8" else float("nan"))
+        for scales in (c.k_scales, c.v_scales):
+            if scales is not None:
+                scales.fill_(float("nan"))
+
+    clear()
+    k, v = (torch.zeros(rows, Hk, M, D, dtype=BF, device=DEV)
+            for _ in range(2))
+    c.begin(range(rows), 0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.append(k, v)
+    gen = torch.Generator().manual_seed(rows + M)
+    want = {}
+    for counts in batches:
+        if counts is None:
+            c.reset()
+            clear()
+            want = {}
+            continue
+        slots = list(range(rows - 1, rows - 1 - len(counts), -1))
+        c.begin(slots, counts)
+        x = [torch.randn(rows * M, Hk, D, generator=gen).to(BF)
+             for _ in range(2)]
+        for t, y in zip((k, v), x):
+            t.copy_(y.view(rows, M, Hk, D).transpose(1, 2))
+        g.replay()
+        at = 0
+        for s, n in zip(slots, counts):
+            old = want.get(s, (torch.empty(0, Hk, D, dtype=BF),) * 2)
+            want[s] = tuple(torch.cat([o, y[at:at + n]])
+                            for o, y in zip(old, x))
+            at += n
+        check_rows(c, want, kv)
