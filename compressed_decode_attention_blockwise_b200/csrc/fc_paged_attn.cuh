@@ -127,12 +127,10 @@ struct PagedCfg {
   static constexpr int kMostCtas = int(WARPS * 2 * kFragment / (NT * 8 * 4));  // of one segment: see the joins
 };
 
-// d += A B, or d = A B + (z0, z1) per column where FIRST (16 x 8 x 16; bf16, or
-// fp16 for int8 pages).
+// d += A B, or d = A B where FIRST (16 x 8 x 16; bf16, or fp16 for int8 pages).
 template <typename T, bool FIRST>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                    float z0 = 0.0f, float z1 = 0.0f) {
-  const float c0 = FIRST ? z0 : d[0], c1 = FIRST ? z1 : d[1], c2 = FIRST ? z0 : d[2], c3 = FIRST ? z1 : d[3];
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  const float c0 = FIRST ? 0.0f : d[0], c1 = FIRST ? 0.0f : d[1], c2 = FIRST ? 0.0f : d[2], c3 = FIRST ? 0.0f : d[3];
   if constexpr (sizeof(T) == 1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%10,%11,%12,%13};"
@@ -172,8 +170,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 // Exact int8 -> fp16 of two codes: x holds 0x6400 | (code + 128) in each half,
-// the fp16 numbers 1024 + code + 128; 1152 is subtracted. (V takes this form: as
-// subnormals like K's, small codes beside large ones lose bits of the output.)
+// the fp16 numbers 1024 + code + 128; 1152 is subtracted. (The codes plus 128 as
+// fp16 subnormals take one instruction less a pair, but then 128 times the sum of
+// the query, or of P, runs through sums that are truncated at its size: 4e-6 to
+// 2.5e-5 of the output for queries that have a mean.)
 __device__ __forceinline__ uint32_t codes_to_f16(uint32_t x) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -474,10 +474,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
     if (rt.len > 0) {
     // query fragments, pre-split into limbs, to this warp's shared memory
     __syncwarp();
-    // int8: K's codes go in as the fp16 subnormals (code + 128) 2^-24 (a byte in
-    // the low half, one permute); what that adds to the scores of heads 2c and
-    // 2c + 1, and what these are scaled by.
-    float qz[NT][2] = {}, qf[NT][2];
+    float qf[NT][2];  // int8: what the scores of heads 2c and 2c + 1 are scaled by
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int g = nt * 8 + r;
@@ -534,34 +531,19 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[i][k] *= up;
         const float down = pow2i(e - 14);
-        qf[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c) * a.scale_log2e * 16777216.0f;
-        qf[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4) * a.scale_log2e * 16777216.0f;
+        qf[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c) * a.scale_log2e;
+        qf[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4) * a.scale_log2e;
       }
-      float used = 0.0f;  // int8: the sum of the query as its limbs hold it
 #pragma unroll
       for (int limb = 0; limb < QL; ++limb)
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (C::ES == 1) {
-              w[e] = take_limb_f16(x[i][2 * e], x[i][2 * e + 1]);
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-              used += f.x + f.y;
-            } else {
-              w[e] = take_limb(x[i][2 * e], x[i][2 * e + 1]);
-            }
-          }
+          for (int e = 0; e < 4; ++e)
+            w[e] = C::ES == 1 ? take_limb_f16(x[i][2 * e], x[i][2 * e + 1]) : take_limb(x[i][2 * e], x[i][2 * e + 1]);
           qs[((limb * NT + nt) * (D / 32) + i) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-      if constexpr (C::ES == 1) {
-        used += __shfl_xor_sync(0xffffffffu, used, 1);
-        used += __shfl_xor_sync(0xffffffffu, used, 2);
-        used *= -128.0f / 16777216.0f;
-        qz[nt][0] = __shfl_sync(0xffffffffu, used, 8 * c);
-        qz[nt][1] = __shfl_sync(0xffffffffu, used, 8 * c + 4);
-      }
     }
     if (a.kn.p && br.count > 0 && end == rt.n && rt.len > 0) {
       // the fused append: the warp with the segment's last tile stores the new
@@ -703,7 +685,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
               } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  ka[u][0][e] = __byte_perm(kr[u][e & 1][ks] ^ 0x80808080u, 0, e < 2 ? 0x4140 : 0x4342);
+                  ka[u][0][e] = codes_to_f16(
+                      __byte_perm(kr[u][e & 1][ks] ^ 0x80808080u, 0x64646464u, e < 2 ? 0x4140 : 0x4342));
               }
             }
 #pragma unroll
@@ -733,8 +716,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
                       continue;
                     }
                     auto& d = kk & 1 ? odd[u][nt] : s[u][nt];
-                    if (kk == 0 && ql == 0 && k == 0) mma<T, true>(d, ka[u][k], b.x, b.y, qz[nt][0], qz[nt][1]);
-                    else if (kk == 1 && ql == 0 && k == 0) mma<T, true>(d, ka[u][k], b.x, b.y);
+                    if (kk <= 1 && ql == 0 && k == 0) mma<T, true>(d, ka[u][k], b.x, b.y);
                     else mma<T, false>(d, ka[u][k], b.x, b.y);
                   }
               }

@@ -1,0 +1,93 @@
+"""How near the paged attention comes to 64 bits, in the 2-norm of each head.
+
+The element-wise bounds of the other tests cover the worst case of every sum;
+the limits here are what a correct kernel's errors add up to when roundings are
+independent, so that a lost limb or a truncated running sum shows.
+
+An fp32 output, per head, relative to its 2-norm. V has mean 1 and deviation 1,
+so sum p |v| is 1.2 times the output and the deviations v - out are as large as
+it; the scores' deviation is 2 (log2 domain: |s| < 16, half a step 2^-21), so at
+200 tokens some six of them carry the sum, sqrt(sum p^2) <= 0.45, and at more
+tokens fewer errors remain. In units of 1e-7:
+  scores   D / 16 + 3 <= 19 roundings whose partial sums are half as large in
+           the mean: sqrt(19 / 3) 2^-22 ln 2 = 4.2; the products of 16 channels
+           are truncated at 2^-23 of sums a quarter as large: 4 of them, 2.7;
+           together 5, times 0.45: 2.2
+  e^x      2^-22 relative, times 0.45: 1.1
+  p        three limbs 2^-24 (int8: two fp16 limbs, 2^-23): 0.3 (0.5)
+  V sums   a tile's three products truncated at 2^-24 in the mean, times 1.2:
+           2.1; at most 170 tiles of one warp added in fp32, the partial sums
+           growing to the whole: sqrt(170 / 3) 2^-24 / sqrt(3) = 2.6
+  l        as the tiles, 2.6; joins and the division: four of 2^-24, 0.7
+Root of the squares: 4.9. The limit is 6. Two limbs of p instead of three leave
+2^-17 / sqrt(3) sqrt(2) 0.45 = 20 at 200 tokens; running sums that stay in the
+tensor cores lose 2^-24 a tile, 100 over 170 tiles.
+"""
+
+import pytest
+import torch
+
+from compressed_decode_attention_blockwise_b200 import PagedKVCache
+from _paged import held
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF, F32 = torch.bfloat16, torch.float32
+LIMIT = 6e-7
+
+
+def shared_cache(k, v, slots, kv, page=64):
+    """A cache all of whose slots share the pages of one sequence, (n, Hk, D)
+    tokens each of K and V."""
+    n, Hk, D = k.shape
+    need = -(-n // page)
+    c = PagedKVCache(1, slots, need, Hk, D, page_size=page, max_pages=need + 1,
+                     kv=kv, token_dtype=k.dtype, device=DEV)
+    c.begin([0], [n])
+    c.append(k.transpose(0, 1)[None], v.transpose(0, 1)[None])
+    table, lens = c.save_map()
+    c.restore_map(table[:1].repeat(slots, 1).contiguous(),
+                  lens[:1].repeat(slots).contiguous())
+    c.begin(range(slots), 0)
+    return c
+
+
+def exact(q, k, v, kv):
+    """(B, Hq, D) in 64 bits; q (B, Hq, 1, D), k and v (n, Hk, D)."""
+    B, Hq, _, D = q.shape
+    Hk = k.shape[1]
+    k, v = held(k, kv), held(v, kv)
+    out = torch.empty(B, Hq, D, dtype=torch.float64, device=q.device)
+    for h in range(Hk):
+        g = slice(h * (Hq // Hk), (h + 1) * (Hq // Hk))
+        s = q[:, g, 0].double() @ k[:, h].T * D ** -0.5
+        out[:, g] = torch.softmax(s, -1) @ v[:, h]
+    return out
+
+
+def off(got, ref):
+    """The largest relative 2-norm of a head's error."""
+    d = (got[:, :, 0].double() - ref).norm(dim=-1)
+    return float((d / ref.norm(dim=-1)).max())
+
+
+def tokens(gen, n, Hk, D, dtype):
+    k = torch.randn(n, Hk, D, generator=gen, device=DEV)
+    v = torch.randn(n, Hk, D, generator=gen, device=DEV) + 1.0
+    return k.to(dtype), v.to(dtype)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("G", [4, 16])
+@pytest.mark.parametrize("qd", [BF, F32])
+def test_int8_queries_with_a_mean(D, G, qd):
+    """Queries whose elements do not average out, and one large channel in K,
+    whose codes leave the others few bits: a score is a small difference of
+    what a bias on the codes would add to it."""
+    gen = torch.Generator(DEV).manual_seed(D + G)
+    k, v = tokens(gen, 2000, 2, D, BF)
+    k[:, :, 5] *= 8.0
+    c = shared_cache(k, v, 4, "i8")
+    q = torch.randn(4, 2 * G, 1, D, generator=gen, device=DEV)
+    q = (1.4 * q + 0.9).to(qd)
+    assert off(c.attention(q), exact(q, k, v, "i8")) <= LIMIT
