@@ -332,7 +332,9 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
   constexpr int KB = C::KL * C::ES, VB = C::VL * C::ES;  // bytes per load
   constexpr int kRow = D * C::ES;                        // bytes of a token's row
   constexpr float kNone = -__builtin_huge_valf();
-  constexpr bool kFine = C::ES != 1 && PL == 3;          // an fp32 result
+  // an fp32 result (int8: of an fp32 query; a bf16 one's eight bits let the sums
+  // of its products be nearly exact, and 6e-7 holds without it)
+  constexpr bool kFine = C::ES == 1 ? QL == 2 : PL == 3;
   extern __shared__ __align__(16) char smem[];
   __shared__ Piece pieces[C::WARPS * 2];
   __shared__ int n_pieces[C::WARPS];

@@ -77,6 +77,18 @@ def tokens(gen, n, Hk, D, dtype):
     return k.to(dtype), v.to(dtype)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kv,qd", [("bf16", BF), ("bf16", F32), ("f32", F32),
+                                   ("i8", BF), ("i8", F32)])
+@pytest.mark.parametrize("n,slots", [(200, 3), (8000, 40), (50000, 8)])
+def test_fp32_results(D, kv, qd, n, slots):
+    gen = torch.Generator(DEV).manual_seed(n + D)
+    k, v = tokens(gen, n, 8, D, F32 if kv == "f32" else BF)
+    c = shared_cache(k, v, slots, kv)
+    q = (2.0 * torch.randn(slots, 16, 1, D, generator=gen, device=DEV)).to(qd)
+    assert off(c.attention(q), exact(q, k, v, kv)) <= LIMIT
+
+
 @pytest.mark.parametrize("D", [32, 64, 128, 256])
 @pytest.mark.parametrize("G", [4, 16])
 @pytest.mark.parametrize("qd", [BF, F32])
