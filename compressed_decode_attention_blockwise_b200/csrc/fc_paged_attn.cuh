@@ -27,7 +27,9 @@
 // products below 2^-24 of the largest dropped. int8 codes are exact in fp16,
 // which takes fewer instructions than bf16 and holds 11 bits a limb: the query
 // (brought to fp16's range by a power of two per head) is one limb, two when
-// it is fp32, and P times V's scale (by a power of two per warp) is two.
+// it is fp32, and P times V's scale (by a power of two per head that follows the
+// running maximum and the products themselves, not the scales: a large V row of
+// little weight leaves the others their bits) is two.
 // Maxima, sums and accumulators are fp32. Sums that stay in the tensor cores'
 // accumulators are truncated, not rounded (7e-6 over 8,000 tokens), so each
 // tile's V products, and for an fp32 result each step's leading score product,
@@ -95,7 +97,6 @@ inline size_t paged_fragment_bytes(int64_t D, int64_t G) {
 #ifdef __CUDACC__
 
 constexpr int kTile = 16;          // tokens per tile
-constexpr float kLazy = 8.0f;      // log2 of how far p may exceed 1
 constexpr int kSetup = 2;          // what beginning a segment costs, in tiles
 constexpr int kJoin = 3;           // what a join over the workspace costs, in tiles per warp
 
@@ -104,6 +105,10 @@ template <typename T, int D_, int NT_, int QL_, int PL_>
 struct PagedCfg {
   static constexpr int D = D_, NT = NT_, QL = QL_, PL = PL_;  // NT: groups of 8 heads
   static constexpr int ES = int(sizeof(T));
+  // log2 of how far p may exceed 1 (int8: the largest scale, 2^121, times it is
+  // a finite fp32 number)
+  static constexpr float kLazy = ES == 1 ? 6.0f : 8.0f;
+  static constexpr float kMostScale = 8.507059173023462e37f;  // 2^126
   static constexpr int KW = D / 4 * ES / 4;   // words of a K row per lane
   static constexpr int VW = D / 8 * ES / 4;   // words of a V row per lane
   static constexpr int KL = 16 / ES < D / 4 ? 16 / ES : D / 4;  // elements per load
@@ -148,6 +153,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 // The exponent of a positive finite x (its floor of log2; subnormals -127).
 __device__ __forceinline__ int exponent_of(float x) { return int(__float_as_uint(x) >> 23) - 127; }
+
+// A power of two g >= 1 that makes up for a factor e in [0, 1], e g <= 1, and
+// leaves x (a power of two) times it at 2^126 or below.
+__device__ __forceinline__ float lower_power(float e, float x) {
+  const int most = 126 - exponent_of(x), k = -1 - exponent_of(e);  // e in [2^(-k - 1), 2^-k)
+  return pow2i(k < 0 ? 0 : k < most ? k : most);
+}
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
@@ -556,8 +568,12 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
     __syncwarp();  // the query's fragments and the new token's rows are visible
     fetch(held + 32, nxt);
 
-    int ve = 0;  // int8: see below
-    float v_most = -1.0f, v_mul = 0.0f, svc[U][2];
+    // int8: a head's accumulators hold sum p v times this power of two, so that
+    // P times V's scale fits fp16; it begins as high as there is one with a
+    // reciprocal in fp32
+    float vm[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) vm[nt][0] = vm[nt][1] = C::kMostScale;
 
     uint32_t kr[U][2][KW / CH] = {}, vr[U][4][VW / CH] = {};
     // where the tiles' halves are: bytes into the layer's pool, scales
@@ -650,7 +666,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
 #pragma unroll 1
     for (int32_t i = C::kPrefetch ? tile - U : tile; i < end; i += U) {
       const bool work = !C::kPrefetch || i >= tile;
-      float s[U][NT][4];
+      float s[U][NT][4], svc[U][2];
       if constexpr (!C::kPrefetch) load_v(i, 0);
       if (work) {
         // ---- S^T = K Q^T
@@ -749,28 +765,10 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
             }
         }
         if constexpr (C::ES == 1) {
-          // V's scales are multiplied into P as 2^(7 - ve) scale, ve above the
-          // exponent of every scale so far, so that fp16 holds them (p <= 2^8)
-          float x = 0.0f;
-#pragma unroll
-          for (int u = 0; u < U; ++u) x = fmaxf(x, fmaxf(fabsf(sv[u][0]), fabsf(sv[u][1])));
-          if (__any_sync(0xffffffffu, x > v_most)) {
-            x = warp_max(x);
-            int e = exponent_of(x) + 1;
-            e = e < -100 ? -100 : e > 120 ? 120 : e;
-            const float f = v_most < 0.0f ? 0.0f : pow2i(ve - e < -126 ? -126 : ve - e);
-            ve = e;
-            v_most = pow2i(e);
-            v_mul = pow2i(7 - e);
-#pragma unroll
-            for (int q = 0; q < C::NQ; ++q)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) acc[q][k] *= f;
-          }
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            svc[u][0] = sv[u][0] * v_mul;  // before the next ones are loaded
-            svc[u][1] = sv[u][1] * v_mul;
+            svc[u][0] = sv[u][0];  // before the next ones are loaded
+            svc[u][1] = sv[u][1];
           }
         }
       }
@@ -790,7 +788,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
 #pragma unroll
             for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(s[u][nt][j], s[u][nt][2 + j]));
             top[nt][j] = x;
-            raise |= x > m[nt][j] + kLazy;
+            raise |= x > m[nt][j] + C::kLazy;
           }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -801,9 +799,16 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
               x = fmaxf(x, m[nt][j]);
-              const float e = join_factor(m[nt][j], x);
+              float e = join_factor(m[nt][j], x);
               m[nt][j] = x;
               l[nt][j] *= e;
+              if constexpr (C::ES == 1) {
+                // what the maximum takes away the scale may give back, or the
+                // tokens before would set the later ones' precision
+                const float g = lower_power(e, vm[nt][j]);
+                vm[nt][j] *= g;
+                e *= g;
+              }
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
                 acc[nt * MT + mt][j] *= e;
@@ -813,7 +818,6 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
         }
 
         // ---- P, and its limbs as B operands (heads x tokens)
-        uint32_t pb[U][PL][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           // no score yet: the maximum is -infinity and p is to be 0
@@ -822,12 +826,63 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
           for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              float p0 = fast_exp2(s[u][nt][2 * hh] - b0), p1 = fast_exp2(s[u][nt][2 * hh + 1] - b1);
+              float& p0 = s[u][nt][2 * hh];
+              float& p1 = s[u][nt][2 * hh + 1];
+              p0 = fast_exp2(p0 - b0);
+              p1 = fast_exp2(p1 - b1);
               l[nt][0] += p0;
               l[nt][1] += p1;
               if constexpr (C::ES == 1) {
                 p0 *= svc[u][hh];
                 p1 *= svc[u][hh];
+              }
+            }
+        }
+        if constexpr (C::ES == 1) {
+          // P times V's scale, in the head's power of two: lowered where a
+          // product passes 2^15, to bring the largest of the tile to [2^7, 2^8)
+          bool low = false;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float x = fmaxf(fabsf(s[0][nt][j]), fabsf(s[0][nt][2 + j]));
+#pragma unroll
+              for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(fabsf(s[u][nt][j]), fabsf(s[u][nt][2 + j])));
+              top[nt][j] = x;
+              low |= top[nt][j] * vm[nt][j] > 32768.0f;
+            }
+          if (__any_sync(0xffffffffu, low)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float x = top[nt][j];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                if (x * vm[nt][j] <= 32768.0f) continue;
+                const int now = 7 - exponent_of(x), e = now - exponent_of(vm[nt][j]);
+                vm[nt][j] = pow2i(now);
+                const float f = pow2i(e < -126 ? -126 : e);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                  acc[nt * MT + mt][j] *= f;
+                  acc[nt * MT + mt][2 + j] *= f;
+                }
+              }
+          }
+        }
+        uint32_t pb[U][PL][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              float p0 = s[u][nt][2 * hh], p1 = s[u][nt][2 * hh + 1];
+              if constexpr (C::ES == 1) {
+                p0 *= vm[nt][0];
+                p1 *= vm[nt][1];
               }
 #pragma unroll
               for (int k = 0; k < PL; ++k) {
@@ -837,7 +892,6 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
                 pb[u][k][nt][hh] = transpose8x8(w);
               }
             }
-        }
 
         // ---- O^T += V^T P^T: the iteration's products in accumulators of their
         // own, added in fp32 (the tensor cores' running sums are truncated)
@@ -909,11 +963,10 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], o);
     if constexpr (C::ES == 1) {
-      const float f = v_most < 0.0f ? 0.0f : pow2i(ve - 7);
 #pragma unroll
       for (int q = 0; q < C::NQ; ++q)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[q][k] *= f;
+        for (int k = 0; k < 4; ++k) acc[q][k] *= pow2i(-exponent_of(vm[q / MT][k & 1]));
     }
     }  // rt.len > 0
     if (tile == 0 && end == rt.n) {

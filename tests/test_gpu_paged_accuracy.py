@@ -103,3 +103,46 @@ def test_int8_queries_with_a_mean(D, G, qd):
     q = torch.randn(4, 2 * G, 1, D, generator=gen, device=DEV)
     q = (1.4 * q + 0.9).to(qd)
     assert off(c.attention(q), exact(q, k, v, "i8")) <= LIMIT
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("first,count", [(0, 1), (0, 40), (333, 1), (700, 60),
+                                         (999, 1)])
+def test_int8_large_values_of_no_weight(D, first, count):
+    """Tokens whose V rows are 2^20 times as large as the others' and whose
+    scores are low by 90 for some heads of the group (they add nothing there)
+    and high for others (they are the result)."""
+    gen = torch.Generator(DEV).manual_seed(first + D)
+    k, v = tokens(gen, 1000, 1, D, F32)
+    base = 2.0 * torch.randn(D, generator=gen, device=DEV)
+    big = slice(first, first + count)
+    k[big] = 0.01 * k[big] - base * (90.0 * D ** 0.5 / float(base @ base))
+    v[big] *= 2.0 ** 20
+    c = shared_cache(k, v, 3, "i8")
+    q = 0.2 * torch.randn(3, 8, 1, D, generator=gen, device=DEV)
+    q[:, ::2] += base
+    q[:, 1::2] -= base
+    ref = exact(q, k, v, "i8")
+    assert float(ref[:, ::2].abs().max()) < 100 < 1e5 < \
+        float(ref[:, 1::2].abs().max())
+    got = c.attention(q)
+    assert off(got[:, ::2], ref[:, ::2]) <= LIMIT
+    # The large tokens' scores are 90, 130 in the log2 domain, where half a step
+    # is 2^-17 and not the 2^-21 that LIMIT counts: D / 16 + 3 roundings of a
+    # score, of which p takes ln 2; ``count`` tokens of nearly equal weight.
+    scores = ((D / 16 + 3) / 3) ** 0.5 * 2.0 ** -17 * 0.6932 / count ** 0.5
+    assert off(got[:, 1::2], ref[:, 1::2]) <= LIMIT + scores
+
+
+def test_int8_scales_over_the_whole_range():
+    """V rows from 2^-100 to 2^100, each the whole result of its own sequence
+    and of the tokens before it."""
+    D = 64
+    gen = torch.Generator(DEV).manual_seed(1)
+    for lo, hi in ((-100, 100), (100, -100), (-100, -100), (100, 100)):
+        k, v = tokens(gen, 120, 1, D, F32)
+        e = torch.linspace(lo, hi, 120, device=DEV).round()
+        v = v * torch.exp2(e)[:, None, None]
+        c = shared_cache(k, v, 1, "i8", page=16)
+        q = torch.randn(1, 4, 1, D, generator=gen, device=DEV)
+        assert off(c.attention(q), exact(q, k, v, "i8")) <= LIMIT
