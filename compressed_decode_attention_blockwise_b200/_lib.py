@@ -59,8 +59,8 @@ EXPORTS = (
     "fc_decode_step_host",
     "fc_pages_reset", "fc_pages_restore", "fc_pages_begin", "fc_pages_fork",
     "fc_pages_free", "fc_pages_crop", "fc_pages_compact", "fc_paged_append",
-    "fc_paged_workspace_bytes", "fc_paged_attention", "fc_paged_step",
-    "fc_paged_read",
+    "fc_paged_workspace_bytes", "fc_paged_capture_id", "fc_paged_attention",
+    "fc_paged_step", "fc_paged_read",
 )
 
 FC_MAX_LAYERS = 16
@@ -223,6 +223,7 @@ def load() -> ctypes.CDLL:
         "fc_paged_append": (ctypes.c_int, [PP, I64, P, P, I32, P, P, I64, I64,
                                            P]),
         "fc_paged_workspace_bytes": (SZ, [I64, I64, I64]),
+        "fc_paged_capture_id": (ctypes.c_uint64, [P]),
         "fc_paged_attention": (ctypes.c_int, [PP, I64, P, I32, P, I64, F32,
                                               I64, I64, P, SZ, P, I32, P, P,
                                               P]),

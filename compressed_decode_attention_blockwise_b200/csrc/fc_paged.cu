@@ -406,6 +406,16 @@ extern "C" size_t fc_paged_workspace_bytes(int64_t Hq, int64_t H, int64_t D) {
   return paged_workspace(D, Hq / H).total;
 }
 
+extern "C" uint64_t fc_paged_capture_id(fc_stream stream) {
+  cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &c, &id) != cudaSuccess) {
+    (void)cudaGetLastError();  // no device: nothing can be capturing
+    return 0;
+  }
+  return c == cudaStreamCaptureStatusNone ? 0 : uint64_t(id) + 1;
+}
+
 extern "C" int fc_paged_attention(const fc_pages* p, int64_t layer, const void* q, int32_t q_dtype,
                                   const int64_t* q_strides, int64_t Hq, float softmax_scale, int64_t window,
                                   int64_t sinks, void* workspace, size_t workspace_bytes, void* out,

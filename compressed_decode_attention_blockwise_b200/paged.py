@@ -100,6 +100,8 @@ class PagedKVCache:
         self._where = device if self._index < 0 else self._index
         self._rows = 0             # rows of the open batch (0: none)
         self._ws: dict = {}        # (stream, Hq) -> workspace
+        self._graph_ws: dict = {}  # the same, of the capture self._capture
+        self._capture = 0
         self._dense: dict = {}     # H -> strides of a dense (rows, H, 1, D)
         self.reset()
 
@@ -316,13 +318,18 @@ class PagedKVCache:
                 return self._attend(q, new, layer, out, softmax_scale, window,
                                     sinks, out_dtype, lse)
         s = self._stream()
+        held = self._ws
         if self._index >= 0 and torch._C._cuda_isCurrentStreamCapturing():
-            # a graph's own: graphs may be replayed side by side
-            ws = self._new_workspace(Hq)
-        else:
-            ws = self._ws.get((s, Hq))
-            if ws is None:
-                ws = self._ws[s, Hq] = self._new_workspace(Hq)
+            # the graph's own: graphs may be replayed side by side. Kept while
+            # it is captured, so that its calls share one zeroing; after that
+            # the graph's memory pool keeps the memory, as any temporary's.
+            capture = self._lib.fc_paged_capture_id(s)
+            if capture != self._capture:
+                self._capture, self._graph_ws = capture, {}
+            held = self._graph_ws
+        ws = held.get((s, Hq))
+        if ws is None:
+            ws = held[s, Hq] = self._new_workspace(Hq)
         if softmax_scale is None:
             softmax_scale = 0.0
         qs = dense if q.is_contiguous() else _I64x4(*q.stride())

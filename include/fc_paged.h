@@ -181,6 +181,14 @@ int fc_paged_append(const fc_pages* p, int64_t layer, const void* k,
 size_t fc_paged_workspace_bytes(int64_t Hq, int64_t H, int64_t D);
 
 /*
+ * fc_paged_capture_id -- a number that no other capture of the process has, of
+ * the capture that `stream` takes part in; 0 when it takes part in none. The
+ * launches that one capture records on one stream run in their order, so they
+ * may share a workspace; those of two captures may not.
+ */
+uint64_t fc_paged_capture_id(fc_stream stream);
+
+/*
  * fc_paged_attention -- attention of one token per row of the open batch over
  * that row's sequence in one layer.
  *   q, out    device, (n_rows, Hq, 1, D); q FC_DTYPE_BF16 or FC_DTYPE_F32, out

@@ -1,5 +1,7 @@
 """Captured launches of the paged cache, replayed after other batches."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -113,3 +115,90 @@ def test_captured_append_writes_every_token(kv, rows, M, batches):
                             for o, y in zip(old, x))
             at += n
         check_rows(c, want, kv)
+
+
+def node_types(g):
+    """The types of a kept graph's nodes (0: kernel, 2: memset)."""
+    cu = ctypes.CDLL("libcuda.so.1")
+    raw, n = ctypes.c_void_p(g.raw_cuda_graph()), ctypes.c_size_t(0)
+    assert cu.cuGraphGetNodes(raw, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cu.cuGraphGetNodes(raw, nodes, ctypes.byref(n)) == 0
+    types = []
+    for x in nodes:
+        t = ctypes.c_int()
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(x), ctypes.byref(t)) == 0
+        types.append(t.value)
+    return types
+
+
+def filled(layers, lens, Hk=2, D=128, page=16):
+    c = PagedKVCache(layers, len(lens), sum(-(-n // page) for n in lens) + 8,
+                     Hk, D, page_size=page, device=DEV)
+    gen = torch.Generator(DEV).manual_seed(sum(lens))
+    c.begin(range(len(lens)), lens)
+    for layer in range(layers):
+        c.append(*(torch.randn(1, Hk, sum(lens), D, generator=gen, device=DEV)
+                   .to(BF) for _ in range(2)), layer=layer)
+    return c, gen
+
+
+def test_a_captured_attention_is_one_launch():
+    """Twelve layers in one graph are twelve kernels and what zeroes their
+    workspace once; the next graph has a workspace of its own."""
+    c, gen = filled(12, [3000, 70, 1])
+    c.begin(range(3), 0)
+    q = torch.randn(12, 3, 8, 1, 128, generator=gen, device=DEV).to(BF)
+    want = [c.attention(q[i], layer=i) for i in range(12)]
+    graphs, outs = [], []
+    for _ in range(2):
+        out = torch.zeros(12, 3, 8, 1, 128, device=DEV)
+        g = torch.cuda.CUDAGraph(keep_graph=True)
+        with torch.cuda.graph(g):
+            for i in range(12):
+                c.attention(q[i], layer=i, out=out[i])
+        types = node_types(g)
+        assert len(types) <= 13 and types.count(0) >= 12
+        g.instantiate()
+        graphs.append(g)
+        outs.append(out)
+    # side by side, eager calls among them
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        assert torch.equal(c.attention(q[0]), want[0])
+    torch.cuda.synchronize()
+    for out in outs:
+        for o, w in zip(out, want):
+            assert torch.equal(o, w)
+
+
+def test_branches_of_one_capture_have_their_own_workspaces():
+    """Two streams of one capture, whose launches may run at once, and two
+    numbers of heads."""
+    c, gen = filled(2, [4000, 900])
+    c.begin([0, 1], 0)
+    q = [torch.randn(2, h, 1, 128, generator=gen, device=DEV).to(BF)
+         for h in (8, 4)]
+    want = [[c.attention(x, layer=i) for x in q] for i in (0, 1)]
+    outs = [[torch.zeros_like(w) for w in ws] for ws in want]
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        for _ in range(10):
+            for x, o in zip(q, outs[0]):
+                c.attention(x, layer=0, out=o)
+            with torch.cuda.stream(side):
+                for x, o in zip(q, outs[1]):
+                    c.attention(x, layer=1, out=o)
+        main.wait_stream(side)
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    for ws, os in zip(want, outs):
+        for w, o in zip(ws, os):
+            assert torch.equal(w, o)
