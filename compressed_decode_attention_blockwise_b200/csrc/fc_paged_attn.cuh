@@ -100,6 +100,15 @@ constexpr int kTile = 16;          // tokens per tile
 constexpr int kSetup = 2;          // what beginning a segment costs, in tiles
 constexpr int kJoin = 3;           // what a join over the workspace costs, in tiles per warp
 
+// What a warp left of a segment (row, head): tiles [from, to) of n.
+struct Piece {
+  int32_t row, head, from, to, n;
+};
+// A segment left to other CTAs as well (row -1: none).
+struct Open {
+  int32_t row, head, cta0, cta1;
+};
+
 // QL, PL: limbs of the query and of P.
 template <typename T, int D_, int NT_, int QL_, int PL_>
 struct PagedCfg {
@@ -128,7 +137,9 @@ struct PagedCfg {
   static constexpr size_t kFragment = size_t(NQ) * 512 + NT * 64;
   static constexpr size_t kQuery = size_t(QL) * NT * (D / 32) * 512;
   static constexpr size_t kShared = WARPS * (2 * kFragment + kQuery);
-  static_assert(kShared + 600 <= 232448, "shared memory of a CTA, with the static arrays");
+  // besides: two pieces and their number for each warp, two open segments
+  static constexpr size_t kStatic = WARPS * (2 * sizeof(Piece) + sizeof(int)) + 2 * sizeof(Open);
+  static_assert(kShared + kStatic <= 232448, "shared memory of a CTA");
   static constexpr int kMostCtas = int(WARPS * 2 * kFragment / (NT * 8 * 4));  // of one segment: see the joins
 };
 
@@ -306,11 +317,6 @@ struct Fragment {
   __device__ __forceinline__ float& l(int h) const { return m(h + C::NT * 8); }
 };
 
-// What a warp left of a segment (row, head): tiles [from, to) of n.
-struct Piece {
-  int32_t row, head, from, to, n;
-};
-
 // Four query elements at q[at ..], of either type and any alignment.
 static __device__ __noinline__ float4 load_query_slow(const void* q, int64_t at, int dtype) {
   return make_float4(load_elem(q, at, dtype), load_elem(q, at + 1, dtype), load_elem(q, at + 2, dtype),
@@ -350,9 +356,6 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
   extern __shared__ __align__(16) char smem[];
   __shared__ Piece pieces[C::WARPS * 2];
   __shared__ int n_pieces[C::WARPS];
-  struct Open {  // a segment left to other CTAs as well (row -1: none)
-    int32_t row, head, cta0, cta1;
-  };
   __shared__ Open open[2];
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31), r = lane >> 2, c = lane & 3;
   char* fragments = smem;  // two per warp
