@@ -288,8 +288,19 @@ def bench_workload(name, peak, W, world, dev, l2, budget_s=0.25):
     return entry
 
 
+LAYER_STEPS = 16    # decode steps of the multi-layer leg
+
+
+def tokens_after_prefill(steps, copies, layers):
+    """Tokens that the legs take behind the prefilled ones: each archive copy
+    its share of the captured steps, then of the end-to-end ones, and one; the
+    layer caches (if any) theirs from the first on."""
+    per_copy = -(-steps // copies)
+    return max(2 * per_copy + 1, LAYER_STEPS if layers > 0 else 0)
+
+
 def bench_layers(w, kd, vd, q_pool, dev, W, world, n_layers=8,
-                 n_steps=16):
+                 n_steps=LAYER_STEPS):
     """Decode steps of n_layers independent layer caches of the workload:
     one fc_decode_step_layers launch per step against n_layers separate
     fc_decode_step launches, each plain and with the overlap flags. CUDA
@@ -376,7 +387,7 @@ def run_fc(args, world, rank, local):
     if arc_bytes < 2 * l2:
         copies = max(copies, 2)
     per_copy = -(-K // copies)
-    extra = 2 * per_copy + 1          # graph steps, then the e2e steps
+    extra = tokens_after_prefill(K, copies, args.layers)
     data = synth.generate(w.replace(steps=extra), q_steps=Q_POOL)
     k_all, v_all = data["k"], data["v"]
     q_pool = data["q"].to(dev)
