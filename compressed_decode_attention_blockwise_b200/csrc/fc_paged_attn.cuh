@@ -342,6 +342,105 @@ __device__ __noinline__ void store_new_rows(const PagedArgs& a, int32_t row, int
   }
 }
 
+// What a warp has of a segment: a lane's accumulators, maxima and sums.
+template <typename C>
+struct Share {
+  float acc[C::NQ][4], m[C::NT][2], l[C::NT][2];
+};
+template <typename C>
+__device__ __forceinline__ void copy_share(float (&acc)[C::NQ][4], float (&m)[C::NT][2], float (&l)[C::NT][2],
+                                           const float (&acc0)[C::NQ][4], const float (&m0)[C::NT][2],
+                                           const float (&l0)[C::NT][2]) {
+#pragma unroll
+  for (int q = 0; q < C::NQ; ++q)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[q][k] = acc0[q][k];
+#pragma unroll
+  for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) m[nt][j] = m0[nt][j], l[nt][j] = l0[nt][j];
+}
+
+// Tiles [tile, end) of a segment once more, token by token in fp32: what the
+// kernel's loop leaves of the heads that have a NaN in a lane, without limbs, so
+// that infinities and NaN act as the formula has them. Some eight times the
+// loop's time.
+template <typename T, typename C>
+__device__ __noinline__ void attend_plain(const PagedArgs& a, int32_t slot, int32_t row, int32_t head,
+                                          const RowTiles& rt, int32_t tile, int32_t end, Share<C>& x) {
+  constexpr int MT = C::D / 16, NT = C::NT;
+  constexpr float kNone = -__builtin_huge_valf();
+  const PageView& pv = a.pages;
+  const int lane = int(threadIdx.x & 31), r = lane >> 2, c = lane & 3;
+  float acc[C::NQ][4], m[NT][2], l[NT][2];
+  copy_share<C>(acc, m, l, x.acc, x.m, x.l);
+  bool redo[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      bool bad = l[nt][j] != l[nt][j];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        bad |= acc[nt * MT + mt][j] != acc[nt * MT + mt][j] || acc[nt * MT + mt][2 + j] != acc[nt * MT + mt][2 + j];
+      redo[nt][j] = (__ballot_sync(0xffffffffu, bad) >> c & 0x11111111u) != 0;
+      if (!redo[nt][j]) continue;
+      m[nt][j] = kNone;
+      l[nt][j] = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) acc[nt * MT + mt][j] = acc[nt * MT + mt][2 + j] = 0.0f;
+    }
+#pragma unroll 1
+  for (int32_t i = tile; i < end; ++i) {
+#pragma unroll 1
+    for (int32_t t = rt.start(i); t < rt.start(i) + kTile; ++t) {
+      const int32_t page = rt.sees(t) ? page_of(pv, slot, t) : -1;
+      if (page < 0) continue;
+      const int64_t at = page * pv.stride_page + head * pv.stride_head + int64_t(t & ((1 << pv.log2P) - 1)) * C::D;
+      float e[NT][2], p[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          // lane r's eighth of the channels, for heads 2c and 2c + 1
+          const int g = nt * 8 + 2 * c + j;
+          float s = 0.0f;
+          if (g < a.G && redo[nt][j]) {
+            const int64_t qh = row * a.q.sb + (int64_t(head) * a.G + g) * a.q.sh + r * (C::D / 8);
+#pragma unroll 1
+            for (int d = 0; d < C::D / 8; ++d) {
+              float k[1];
+              load_elems<T, 1>(reinterpret_cast<const T*>(pv.k) + at + r * (C::D / 8) + d, k);
+              s += k[0] * load_elem(a.q.p, qh + d, a.q_dtype);
+            }
+          }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (!redo[nt][j]) continue;
+          s *= a.scale_log2e;
+          const float top = fmaxf(m[nt][j], s);
+          e[nt][j] = join_factor(m[nt][j], top);
+          p[nt][j] = fast_exp2(s - (top == kNone ? 0.0f : top));
+          m[nt][j] = top;
+          l[nt][j] = l[nt][j] * e[nt][j] + (r == 0 ? p[nt][j] : 0.0f);  // (summed over the lanes later)
+        }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int idx = 2 * mt, d = idx / C::VL * 8 * C::VL + r * C::VL + idx % C::VL;
+        float v[2];
+        load_elems<T, 2>(reinterpret_cast<const T*>(pv.v) + at + d, v);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (redo[nt][k & 1])
+              acc[nt * MT + mt][k] = acc[nt * MT + mt][k] * e[nt][k & 1] + p[nt][k & 1] * v[k >> 1];
+      }
+    }
+  }
+  copy_share<C>(x.acc, x.m, x.l, acc, m, l);
+}
+
 template <typename T, int D, int NT, int QL, int PL>
 __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
     paged_attention_kernel(const __grid_constant__ PagedArgs a) {
@@ -956,6 +1055,25 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NT, QL, PL>::WARPS * 32, 1)
         }
       }
       if constexpr (C::kPrefetch) load_v(i + U, 0);
+    }
+
+    // ---- an infinity's limbs (inf - inf, or inf times a limb that is 0) are NaN
+    // where its products are not: heads with a NaN are done again without limbs.
+    // (An int8 row with one reads as NaN.)
+    if constexpr (C::ES != 1) {
+      bool bad = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) bad |= l[nt][0] != l[nt][0] || l[nt][1] != l[nt][1];
+#pragma unroll
+      for (int q = 0; q < C::NQ; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) bad |= acc[q][k] != acc[q][k];
+      if (__any_sync(0xffffffffu, bad)) {
+        Share<C> x;  // (through memory: the loop's registers stay its own)
+        copy_share<C>(x.acc, x.m, x.l, acc, m, l);
+        attend_plain<T, C>(a, br.slot, row, head, rt, tile, end, x);
+        copy_share<C>(acc, m, l, x.acc, x.m, x.l);
+      }
     }
 
     // ---- the segment's sums over the lanes' tokens; whole segments are done

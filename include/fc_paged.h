@@ -18,6 +18,10 @@
  *   seen(t) = t < n and (window == 0 or t >= n - window or t < sinks)
  *   s_t = sigma q.k_t,  m = max s_t,  l = sum e^(s_t - m),
  *   out = sum e^(s_t - m) v_t / l,  lse = m + ln l   over the seen t.
+ * An infinity or a NaN in a query or in a seen row acts as the formula has it in
+ * fp32 (a score of -infinity is a token without weight, an infinite element of V
+ * an infinite output of its channel) and stays in its row and kv head. int8 rows
+ * with one read as NaN, and an int8 head whose query has one is NaN.
  * The tokens of all sequences are split evenly over the GPU; the parts of one
  * sequence are joined in a fixed order, so equal inputs give equal bits.
  *
@@ -200,8 +204,8 @@ uint64_t fc_paged_capture_id(fc_stream stream);
  *   workspace >= fc_paged_workspace_bytes, 256-byte aligned, all zero before
  *             its first use; every call leaves it fit for the next. Calls
  *             that share one must not overlap on the GPU.
- * A row that sees no token (padding, an empty sequence) gives out = 0 and
- * lse = -infinity. Masked tokens are not read. One kernel launch.
+ * A row that sees no token (padding, an empty sequence), or only tokens whose
+ * scores are -infinity, gives out = 0 and lse = -infinity. Masked tokens are not read. One kernel launch.
  */
 int fc_paged_attention(const fc_pages* p, int64_t layer, const void* q,
                        int32_t q_dtype, const int64_t* q_strides, int64_t Hq,

@@ -28,7 +28,7 @@ import pytest
 import torch
 
 from compressed_decode_attention_blockwise_b200 import PagedKVCache
-from _paged import held
+from _paged import attend, attend_bound, held
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -146,3 +146,103 @@ def test_int8_scales_over_the_whole_range():
         c = shared_cache(k, v, 1, "i8", page=16)
         q = torch.randn(1, 4, 1, D, generator=gen, device=DEV)
         assert off(c.attention(q), exact(q, k, v, "i8")) <= LIMIT
+
+
+def with_nonfinite(kv, D, qd, lens, edit, fused=False):
+    """(output before, output after, q, k, v of slot 1) of a cache of two kv
+    heads and eight query heads in which ``edit`` has changed q, k and v of
+    slot 1 (fused: its last token comes by a step)."""
+    gen = torch.Generator(DEV).manual_seed(D + lens[1])
+    tok = F32 if kv == "f32" else BF
+    k, v = tokens(gen, sum(lens), 2, D, tok)
+    q = torch.randn(len(lens), 8, 1, D, generator=gen, device=DEV).to(qd)
+    outs = []
+    for changed in (False, True):
+        if changed:
+            at = slice(lens[0], lens[0] + lens[1])
+            edit(q[1], k[at], v[at])
+        c = PagedKVCache(1, len(lens), sum(lens) // 16 + 9, 2, D, kv=kv,
+                         token_dtype=tok, device=DEV)
+        c.begin(range(len(lens)), lens)
+        c.append(k.transpose(0, 1)[None], v.transpose(0, 1)[None])
+        if fused:
+            last = torch.tensor(lens).cumsum(0) - 1
+            for s in range(len(lens)):
+                c.crop(s, -1)
+            c.begin(range(len(lens)))
+            outs.append(c.step(q, k[last][:, :, None], v[last][:, :, None]))
+        else:
+            c.begin(range(len(lens)), 0)
+            outs.append(c.attention(q))
+    return outs[0], outs[1], q[1], k[at], v[at]
+
+
+def check_heads(got, q, k, v, heads, drop=None):
+    """Heads of slot 1 against the plain form over the tokens but ``drop``;
+    got (8, 1, D), channels that are not finite in v set to 0 there."""
+    keep = [t for t in range(k.shape[0]) if t != drop]
+    f = lambda x: x.double().cpu().numpy()
+    D = q.shape[-1]
+    v = torch.where(v.isfinite(), v, torch.zeros_like(v))
+    k, v = k[keep], v[keep]
+    ref, _, mag, dots = attend(f(q[:, 0]), f(k), f(v), 4, D ** -0.5)
+    err = abs(f(got[:, 0]) - ref)
+    ok = err <= attend_bound(mag, dots, ref, len(keep), D, F32)
+    return ok[heads]
+
+
+@pytest.mark.parametrize("kv,qd", [("bf16", BF), ("bf16", F32), ("f32", F32)])
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("lens,at", [([300, 77, 130], 50), ([40, 1, 9], 0),
+                                     ([9, 20011], 12345), ([300, 33, 5], 32)])
+def test_infinite_values_are_the_formulas(kv, D, qd, lens, at):
+    """An infinity in a seen K row is a score of minus or plus infinity (a
+    token without weight; NaN), one in V an infinite output of its channel;
+    the other channels, heads and rows have the values of the formula."""
+    def k_edit(q, k, v):
+        q[:, 0, 9] = q[:, 0, 9].abs() * torch.tensor(
+            [1, 1, -1, 1, -1, 1, -1, 1], device=DEV, dtype=q.dtype)
+        k[at, 1, 9] = float("-inf")
+    old, got, q, k, v = with_nonfinite(kv, D, qd, lens, k_edit,
+                                       fused=at == lens[1] - 1)
+    rest = torch.ones(len(lens), 8, dtype=torch.bool, device=DEV)
+    rest[1] = False
+    assert torch.equal(got[rest], old[rest])
+    assert got[1, [4, 6]].isnan().all()              # a score of +inf
+    if lens[1] > 1:                                   # -inf: without the token
+        assert check_heads(got[1], q, k, v, [5, 7], drop=at).all()
+    assert check_heads(got[1], q, torch.nan_to_num(k), v, [0, 1, 2, 3]).all()
+
+    def v_edit(q, k, v):
+        v[at, 1, 9] = float("-inf")
+        v[at, 0, 3] = float("inf")
+    old, got, q, k, v = with_nonfinite(kv, D, qd, lens, v_edit,
+                                       fused=at == lens[1] - 1)
+    assert torch.equal(got[rest], old[rest])
+    assert (got[1, 4:, 0, 9] == float("-inf")).all()
+    assert (got[1, :4, 0, 3] == float("inf")).all()
+    ok = check_heads(got[1], q, k, v, list(range(8)))
+    ok[4:, 9] = ok[:4, 3] = True
+    assert ok.all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f32", "i8"])
+@pytest.mark.parametrize("what", ["k", "v", "q"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_nonfinite_elements_stay_in_their_head(kv, what, bad):
+    """A NaN (int8: or an infinity) in a seen row makes NaN of the outputs of
+    its (row, kv head), or of its channel of them in V; one in a query of those
+    of its head. All others keep their bits."""
+    def edit(q, k, v):
+        if what == "q":
+            q[6, 0, 9] = bad
+        else:
+            (k if what == "k" else v)[50, 1, 9] = bad
+    old, got, *_ = with_nonfinite(kv, 64, F32 if kv == "f32" else BF,
+                                  [300, 77, 130], edit)
+    head = torch.zeros(3, 8, dtype=torch.bool, device=DEV)
+    head[1, 6 if what == "q" else slice(4, 8)] = True
+    assert torch.equal(got[~head], old[~head])
+    if bad != bad or kv == "i8":
+        x = got[head][..., 9] if what == "v" and kv != "i8" else got[head]
+        assert x.isnan().all()
