@@ -147,7 +147,10 @@ class PagedKVCache:
         """Open the batch of a step: row i is ``slots[i]``, which grows by
         ``counts[i]`` tokens (an int for all rows; one each by default).
         Missing pages are taken, a shared last page is copied first. ``rows``
-        pads the batch with empty rows (for a captured graph of fixed size).
+        pads the batch with empty rows (for a captured graph of fixed size;
+        a captured ``append`` writes no more tokens than it was given at its
+        capture, a captured ``step`` one in a row: the batches it is replayed
+        for may not have more).
         Raises FcError with FC_ERR_CAPACITY, nothing changed, when the pages
         do not suffice."""
         slots = _ints(slots)

@@ -37,8 +37,13 @@
  *   - The batch of the current step (fc_pages_begin) is device data too, so a
  *     captured graph of fc_paged_append / _attention / _step launches may be
  *     replayed after each fc_pages_begin with at most as many rows (the rows
- *     past them are then empty). A replay without a new batch repeats the last
- *     one: it must not follow a fork, free or crop of its slots.
+ *     past them are then empty), with at most as many new tokens as a captured
+ *     append was offered (B * M), and with at most one in each row where a step
+ *     was captured (a row with none attends only). A replay cannot refuse:
+ *     tokens beyond these count as present, and nothing has written them. A
+ *     captured fc_paged_read has the slot's length of its call. A replay without
+ *     a new batch repeats the last one: it must not follow a fork, free or crop
+ *     of its slots, or a restore.
  *   - Queue all calls of one cache on one stream, or order the streams.
  *
  * Supported sizes: D in {32, 64, 128, 256}; Hq a multiple of H with G = Hq / H
@@ -167,7 +172,9 @@ int fc_pages_compact(fc_pages* p, int64_t* n_live, fc_stream stream);
  *   k, v      device, (B, H, M, D) of dtype with element strides [4],
  *             innermost 1: new token j of the batch (rows in order, each
  *             row's tokens in order) is element (j / M, :, j mod M, :).
- *             B * M >= the batch's new tokens; further elements are ignored.
+ *             B * M >= the batch's new tokens; further elements are ignored
+ *             (a captured launch writes as many of later batches as they have,
+ *             up to B * M).
  *   dtype     the pages' dtype; FC_DTYPE_BF16 or FC_DTYPE_F32 for int8 pages.
  * int8 pages: scale = max_d |x| / 127 in fp32, code = x / (max_d |x| / 127)
  * rounded to nearest, ties to even, decided exactly; an all-zero row stores

@@ -202,3 +202,42 @@ def test_branches_of_one_capture_have_their_own_workspaces():
     for ws, os in zip(want, outs):
         for w, o in zip(ws, os):
             assert torch.equal(w, o)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+def test_a_captured_step_attends_for_rows_without_a_token(kv):
+    """A step captured over one token a row, replayed for a batch in which some
+    rows have none: those rows only attend, and nothing of theirs is written."""
+    c = PagedKVCache(1, 4, 60, 2, 64, kv=kv, device=DEV)
+    gen = torch.Generator(DEV).manual_seed(9)
+    lens = [33, 160, 16, 5]
+    c.begin(range(4), lens)
+    c.append(*(torch.randn(1, 2, sum(lens), 64, generator=gen, device=DEV)
+               .to(BF) for _ in range(2)))
+    q, k, v = (torch.randn(4, h, 1, 64, generator=gen, device=DEV).to(BF)
+               for h in (8, 2, 2))
+    out = torch.zeros(4, 8, 1, 64, device=DEV)
+    c.begin(range(4))
+    c.step(q, k, v, out=out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.step(q, k, v, out=out)
+    for counts in ([1, 0, 1, 0], [0, 0, 0, 0], [0, 1]):
+        slots = list(range(len(counts)))
+        before = [c.read(s) for s in range(4)]
+        c.begin(slots, counts)
+        k.add_(0.5)
+        g.replay()
+        want = c.attention(q[:len(counts)].contiguous())
+        assert torch.equal(out[:len(counts)], want)
+        assert not out[len(counts):].any()
+        for s in range(4):
+            n = before[s][0].shape[2]
+            new = counts[s] if s < len(counts) else 0
+            after = c.read(s)
+            assert after[0].shape[2] == n + new
+            for a, b in zip(after, before[s]):
+                assert torch.equal(a[:, :, :n], b)
+            if new and kv == "bf16":
+                assert torch.equal(after[0][0, :, n], k[s, :, 0])
+                assert torch.equal(after[1][0, :, n], v[s, :, 0])
