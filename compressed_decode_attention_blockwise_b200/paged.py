@@ -46,7 +46,9 @@ class PagedKVCache:
         self.Hk, self.D, self.page_size = Hk, D, page_size
         self.max_pages = max_pages or n_pages
         self.kv = kv
-        store = _STORE[kv]
+        store = _STORE.get(kv)
+        if store is None:
+            raise ValueError('kv must be "bf16", "f32" or "i8"')
         if kv != "i8":
             token_dtype = store
         if token_dtype not in (torch.bfloat16, torch.float32):
