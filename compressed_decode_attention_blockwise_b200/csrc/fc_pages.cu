@@ -7,6 +7,7 @@
 // copy call, nothing that the host could change before the GPU has read it.
 // Page copies are one pass over the moved pages of all layers, a warp per
 // 4 KB piece of one head's run, so they are bound by HBM (read + write).
+#include <memory>
 #include <new>
 #include <utility>
 #include <vector>
@@ -512,11 +513,11 @@ extern "C" int fc_pages_restore(fc_pages* p, const int32_t* table, const int32_t
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (cudaMemsetAsync(p->table, 0xff, size_t(p->n_slots) * size_t(p->max_pages) * 4, cs) != cudaSuccess)
       return FC_ERR_CUDA;
-    std::vector<MapUpload> up(1, MapUpload(p, cs));  // 28 KB: kept off the stack
-    int st = up[0].add(-1, lens, p->n_slots);
+    const std::unique_ptr<MapUpload> up(new MapUpload(p, cs));  // 28 KB: kept off the stack
+    int st = up->add(-1, lens, p->n_slots);
     for (int64_t s = 0; s < p->n_slots && st == FC_OK; ++s)
-      st = up[0].add(int32_t(s), table + s * p->max_pages, pages_for(p, lens[s]));
-    if (st == FC_OK) st = up[0].flush();
+      st = up->add(int32_t(s), table + s * p->max_pages, pages_for(p, lens[s]));
+    if (st == FC_OK) st = up->flush();
     if (st != FC_OK) return st;
     for (int64_t s = 0; s < p->n_slots; ++s) {
       const int64_t n = pages_for(p, lens[s]);
