@@ -367,7 +367,7 @@ __device__ __forceinline__ void copy_share(float (&acc)[C::NQ][4], float (&m)[C:
 // loop's time.
 template <typename T, typename C>
 __device__ __noinline__ void attend_plain(const PagedArgs& a, int32_t slot, int32_t row, int32_t head,
-                                          const RowTiles& rt, int32_t tile, int32_t end, Share<C>& x) {
+                                          RowTiles rt, int32_t tile, int32_t end, Share<C>& x) {
   constexpr int MT = C::D / 16, NT = C::NT;
   constexpr float kNone = -__builtin_huge_valf();
   const PageView& pv = a.pages;
