@@ -33,14 +33,16 @@
 // Maxima, sums and accumulators are fp32. Sums that stay in the tensor cores'
 // accumulators are truncated, not rounded (7e-6 over 8,000 tokens), so each
 // tile's V products, and for an fp32 result each step's leading score product,
-// are added in fp32. Against 64 bits: 3e-7 in fp32, the output's own rounding in
+// are added in fp32 (int8: for an fp32 query). Against 64 bits, in the 2-norm of a
+// head: 6e-7 and less in fp32 for scores below 2^4 (log2 domain; beyond that a
+// score's own half step shows), 1.4e-7 over a batch; the output's own rounding in
 // bf16.
 //
 // Measured (B200, calls back to back): one bf16 sequence of 131,075 tokens, 32
-// query and 8 kv heads of 128: 88 to 91 us, 5.9 TB/s, 0.90 of the copy rate. 64
-// int8 sequences of up to 8,199 tokens, 64 / 8 heads: 163 to 169 us, 4.2 TB/s,
-// bound by its 467 instructions per tile. One fp32 sequence of 256 tokens, 4 heads of 64:
-// 9.5 us, all latency.
+// query and 8 kv heads of 128: 90 to 91 us, 5.9 TB/s, 0.90 of the copy rate. 64
+// int8 sequences of up to 8,199 tokens, 64 / 8 heads: 172 us, 4.1 TB/s, bound by
+// its 503 instructions per tile. One fp32 sequence of 256 tokens, 4 heads of 64:
+// 9.7 us, all latency.
 //
 // Softmax: each warp keeps its own running maximum per head and raises it only
 // when a tile exceeds it by more than 2^8 (a vote); until then p <= 2^8 and the
@@ -123,7 +125,8 @@ struct PagedCfg {
   static constexpr int KL = 16 / ES < D / 4 ? 16 / ES : D / 4;  // elements per load
   static constexpr int VL = 16 / ES < D / 8 ? 16 / ES : D / 8;
   // tiles per iteration: more than one only where a tile is a few loads (two for
-  // int8 rows of 128 spilled: 250 us against 195 for 64 sequences of 8K)
+  // int8 rows of 128 spilled far more than one's 16 bytes: 250 us against 195 for
+  // 64 sequences of 8K; one for int8 rows of 64: 104 us against 96)
   static constexpr int U = KW >= 8 ? 1 : 2;
   // Rows too wide for the registers are taken in parts (two, or four), and only
   // the first part of K and of V is loaded ahead. fp32 and int8 rows need room
@@ -133,6 +136,9 @@ struct PagedCfg {
   static constexpr int CH = kRegs <= (ES == 2 ? 192 : 160) ? 1 : NT * D / 4 + 2 * U * KW <= (ES == 4 ? 176 : 192) ? 2 : 4;
   static constexpr bool kPrefetch = CH == 1;
   static constexpr int NQ = NT * D / 16;      // float4 accumulators per lane
+  // 16 warps of 128 registers where a tile needs few (bf16 rows of 64: 5.1 TB/s
+  // with 12, 5.5 with 16; int8 rows of 64 spill 132 bytes with 16 and none with
+  // 12: 96 and 97 us for 64 sequences of 8K)
   static constexpr int WARPS = NQ >= 32 ? 4 : NQ >= 16 || kRegs > 96 ? 8 : kRegs > 48 || NT > 1 ? 12 : 16;
   static constexpr size_t kFragment = size_t(NQ) * 512 + NT * 64;
   static constexpr size_t kQuery = size_t(QL) * NT * (D / 32) * 512;
